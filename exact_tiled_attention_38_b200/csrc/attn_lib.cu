@@ -9,6 +9,11 @@
 //                        (d = 128, groups 2..32): plan, stream, gather
 //   generic_fwd.cuh      prefill and decode for the other head sizes
 //   merge.cuh            LSE merge of partial results (context parallelism)
+// The paged-cache operators have their boundary in paged_api.cuh:
+//   paged_sm100.cuh      attention of new tokens over pages (tcgen05, TMA)
+//   paged_generic.cuh    the same for the other sizes (CUDA cores)
+//   rope.cuh             rotary positions, and their append to the cache
+//   pages.cuh            page update and compaction
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -17,13 +22,18 @@
 #include <cstdint>
 #include <mutex>
 #include <type_traits>
+#include <utility>
 
 #include "../../include/attn.h"
 #include "decode_ps_sm100.cuh"
 #include "decode_sm100.cuh"
 #include "generic_fwd.cuh"
 #include "merge.cuh"
+#include "paged_generic.cuh"
+#include "paged_sm100.cuh"
+#include "pages.cuh"
 #include "prefill_sm100.cuh"
+#include "rope.cuh"
 
 namespace eta {
 namespace api {
@@ -871,6 +881,9 @@ const char* attn_strerror(int code) {
       return "attn_decode_noalloc: one split of the CUDA-core decode pass (B * Hq * (d + 1) "
              "floats, plus B int64 token offsets above 1024 sequences) exceeds its fixed array "
              "of 2,097,152 floats";
+    case ATTN_ERR_PAGES:
+      return "a paged-cache operator met a page id outside the pool, a length beyond the table, "
+             "bad row offsets or a bad source row; what it gave for that sequence is undefined";
     default:
       return "unknown error code";
   }
@@ -887,7 +900,8 @@ int attn_get_device_status(attn_stream_t stream, unsigned int* raw_code) {
       return ATTN_ERR_CUDA;
   }
   if (raw_code != nullptr) *raw_code = v;
-  return v == 0 ? ATTN_OK : ATTN_ERR_TIMEOUT;
+  if (v == 0) return ATTN_OK;
+  return (v & eta::paged::kStatusPages) != 0 ? ATTN_ERR_PAGES : ATTN_ERR_TIMEOUT;
 }
 
 int attn_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B,
@@ -1143,3 +1157,5 @@ extern "C" int attn_decode_noalloc(const void* q, const void* kcache, const void
                                                      Hkv, d, scale,
                                                      reinterpret_cast<cudaStream_t>(stream));
 }
+
+#include "paged_api.cuh"

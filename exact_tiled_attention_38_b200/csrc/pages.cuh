@@ -1,0 +1,382 @@
+// Page operations of a paged cache: rows taking over other rows (forks, beam
+// steps, ended and new sequences) and growing, and compaction of the live
+// pages. Both first settle the whole numbers (block tables, reference counts,
+// which page goes where) in one cluster of CTAs, whose hardware barrier stands
+// between the steps, then copy page contents with the whole grid.
+//
+// Free pages are those with a reference count <= 0, and are always taken
+// lowest first in the order of the rows, so the result does not depend on
+// timing: atomic additions and minima of whole numbers only.
+//
+// update: row b of the next state goes on from row source[b] of this one
+// (-1: from nothing) and grows by add[b] tokens. Rows that share a source share
+// its full pages. Its last, partly filled page stays with one of them -- the
+// source row itself if it goes on, else the first that takes it over -- and the
+// others get a copy in a page of their own.
+// compact: with n live pages, those at n and above move, in order, into the
+// free pages below n, in order: the fewest copies, and no page is both read
+// and written, so the copies need no order among them.
+//
+// Bound: the whole numbers by latency (a few dependent passes over the tables
+// and the counts, which stay in L2), the contents by memory (each moved page is
+// read once and written once). One cluster of 8 CTAs keeps the steps in one
+// launch; a barrier of its CTAs costs about a microsecond.
+#pragma once
+
+#include <climits>
+
+#include "paged_common.cuh"
+
+namespace eta {
+namespace pages {
+
+constexpr int kCtas = 8;
+constexpr int kThreads = 1024;
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 4;
+constexpr int kCopyBytes = kCopyThreads * 16 * kCopyUnroll;  // one CTA's piece of a copy
+
+__device__ __forceinline__ int cta_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return static_cast<int>(r);
+}
+
+// Barrier of the cluster's threads. Release / acquire at cluster scope: what
+// any thread wrote to global memory before it, every thread sees after it.
+__device__ __forceinline__ void cluster_barrier() {
+  __threadfence();
+  __syncthreads();  // (every warp converged, as the aligned form asks)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Reads and writes of data that other CTAs of the cluster write in the same
+// launch go past L1.
+__device__ __forceinline__ int ld(const int* p) { return __ldcg(p); }
+__device__ __forceinline__ void st(int* p, int v) { __stcg(p, v); }
+
+// Exclusive prefix of v over the block's threads; *total gets the sum. `red`
+// holds 33 words.
+__device__ __forceinline__ int block_scan(int v, int* red, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // red's last use
+  if (lane == 31) red[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int w = red[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    red[lane] = w;
+  }
+  __syncthreads();
+  *total = red[31];
+  return x - v + (warp > 0 ? red[warp - 1] : 0);
+}
+
+struct Params {
+  const int* table;  // [B][width]
+  const int* lens;
+  const int* refs;   // [P]
+  const int* source;
+  const int* add;
+  int* table_out;
+  int* lens_out;
+  int* refs_out;
+  int* info;      // [2]
+  int B, width, P, page_log2;
+  // workspace
+  int* keeper;    // [B]: update: the row (-1: the source itself) that keeps a source's last page
+  int* need_off;  // [B + 1]: update: prefix of the fresh pages of each row
+  int* counts;    // [kCtas]: free pages of each CTA's share
+  int* list;      // [P]: free pages in order; compact: destination of move k
+  int* from;      // [max(B, P)] sources, and
+  int* to;        // destinations of the copies
+  int* n_copies;  // [1]
+};
+
+__device__ __forceinline__ int ceil_pages(int len, int log2) {
+  return static_cast<int>((static_cast<long long>(len) + (1 << log2) - 1) >> log2);
+}
+
+// One row of an update: what it goes on from and what it keeps.
+struct Row {
+  int s;      // source row, -1: none
+  int L;      // its tokens
+  int longer; // tokens after growing
+  int held;   // pages of the source
+  int kept;   // pages of them that this row keeps as they are
+  int want;   // pages after growing
+  bool copy;  // the source's last page is copied into this row's first fresh page
+};
+
+__device__ __forceinline__ int clamp_len(int l, const Params& p) {
+  const long long cap = static_cast<long long>(p.width) << p.page_log2;
+  return static_cast<int>(min(static_cast<long long>(max(l, 0)), cap));
+}
+
+__device__ __forceinline__ Row row_of(const Params& p, int b) {
+  Row r;
+  const int s = p.source[b];
+  r.s = (s >= 0 && s < p.B) ? s : -1;
+  r.L = r.s >= 0 ? clamp_len(p.lens[r.s], p) : 0;
+  const long long longer = static_cast<long long>(r.L) + max(p.add[b], 0);
+  r.longer = static_cast<int>(min(longer, static_cast<long long>(INT_MAX)));
+  r.held = ceil_pages(r.L, p.page_log2);
+  r.want = ceil_pages(r.longer, p.page_log2);
+  const int full = r.L >> p.page_log2;
+  const bool keeps = r.s >= 0 && ld(p.keeper + r.s) == (r.s == b ? -1 : b);
+  r.kept = keeps ? r.held : full;
+  r.copy = r.held > r.kept;
+  return r;
+}
+
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
+    pages_update_kernel(const Params p) {
+  __shared__ int red[33];
+  const int rank = cta_rank(), tid = threadIdx.x;
+  const int all = kCtas * kThreads, me = rank * kThreads + tid;
+  const int lane = tid & 31, wid = me >> 5, warps = all >> 5;
+  paged::grid_launch_dependents();
+
+  // 1. The outputs start as the inputs; no row keeps a last page yet.
+  for (int i = me; i < p.P; i += all) st(p.refs_out + i, p.refs[i]);
+  for (int b = me; b < p.B; b += all) st(p.keeper + b, INT_MAX);
+  if (me == 0) st(p.n_copies, 0);
+  cluster_barrier();
+
+  // 2. Every row lets go of its pages; the rows that take a source over find
+  // out which of them keeps its last page.
+  for (int b = wid; b < p.B; b += warps) {
+    const int len = p.lens[b], L = clamp_len(len, p), n = ceil_pages(L, p.page_log2);
+    if (lane == 0) {
+      if (len > L) paged::bad(paged::kBadLength);
+      const int s = p.source[b];
+      if (s >= 0 && s < p.B)
+        atomicMin(p.keeper + s, s == b ? -1 : b);
+      else if (s != -1)
+        paged::bad(paged::kBadSource);
+    }
+    for (int j = lane; j < n; j += 32) {
+      const int page = p.table[static_cast<size_t>(b) * p.width + j];
+      if (page >= 0 && page < p.P)
+        atomicAdd(p.refs_out + page, -1);
+      else
+        paged::bad(paged::kBadPage);
+    }
+  }
+  cluster_barrier();
+
+  // 3. Every row holds the pages that it keeps. CTA 0 meanwhile sums up the
+  // fresh pages that the rows need.
+  for (int b = wid; b < p.B; b += warps) {
+    const Row r = row_of(p, b);
+    for (int j = lane; j < r.kept; j += 32) {
+      const int page = p.table[static_cast<size_t>(r.s) * p.width + j];
+      if (page >= 0 && page < p.P) atomicAdd(p.refs_out + page, 1);
+    }
+  }
+  if (rank == 0) {
+    int too_long = 0, sum = 0;
+    const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    for (int b = b0; b < b1; ++b) {
+      const Row r = row_of(p, b);
+      if (r.want > p.width)
+        ++too_long;  // the row's tokens do not fit its table
+      else
+        sum += r.want - r.kept;
+    }
+    int total, longs;
+    block_scan(too_long, red, &longs);
+    int run = block_scan(sum, red, &total);
+    for (int b = b0; b < b1; ++b) {
+      const Row r = row_of(p, b);
+      st(p.need_off + b, run);
+      if (r.want <= p.width) run += r.want - r.kept;
+    }
+    if (tid == 0) {
+      st(p.need_off + p.B, total);
+      st(p.info + 1, longs);
+    }
+  }
+  cluster_barrier();
+
+  // 4. Free pages, counted per thread's share of the pool.
+  const int per = (p.P + all - 1) / all;
+  const int p0 = static_cast<int>(min(static_cast<long long>(p.P), static_cast<long long>(me) * per));
+  const int p1 = min(p.P, p0 + per);
+  int mine = 0, cta_total;
+  for (int i = p0; i < p1; ++i) mine += ld(p.refs_out + i) <= 0;
+  int at = block_scan(mine, red, &cta_total);
+  if (tid == 0) st(p.counts + rank, cta_total);
+  cluster_barrier();
+  int free_all = 0;
+  for (int r = 0; r < kCtas; ++r) {
+    const int c = ld(p.counts + r);
+    if (r < rank) at += c;
+    free_all += c;
+  }
+  const int need = ld(p.need_off + p.B);
+  const bool refused = need > free_all || ld(p.info + 1) > 0;
+  if (me == 0) st(p.info, max(need - free_all, 0));
+  if (!refused)
+    for (int i = p0; i < p1 && at < need; ++i)
+      if (ld(p.refs_out + i) <= 0) st(p.list + at++, i);
+  cluster_barrier();
+
+  // 5. The new tables.
+  for (int b = wid; b < p.B; b += warps) {
+    const Row r = row_of(p, b);
+    int* out = p.table_out + static_cast<size_t>(b) * p.width;
+    if (refused) {  // everything stays as it was
+      const int* in = p.table + static_cast<size_t>(b) * p.width;
+      for (int j = lane; j < p.width; j += 32) out[j] = in[j];
+      if (lane == 0) p.lens_out[b] = p.lens[b];
+      continue;
+    }
+    const int first = ld(p.need_off + b);
+    const int* in = p.table + static_cast<size_t>(max(r.s, 0)) * p.width;
+    for (int j = lane; j < p.width; j += 32) {
+      int page = -1;
+      if (j < r.kept) {
+        page = in[j];
+      } else if (j < r.want) {
+        page = ld(p.list + first + j - r.kept);
+        st(p.refs_out + page, 1);
+        if (r.copy && j == r.kept) {
+          const int of = in[j];
+          if (of >= 0 && of < p.P) {
+            const int k = atomicAdd(p.n_copies, 1);
+            p.from[k] = of;
+            p.to[k] = page;
+          }
+        }
+      }
+      out[j] = page;
+    }
+    if (lane == 0) p.lens_out[b] = r.longer;
+  }
+  if (refused)
+    for (int i = me; i < p.P; i += all) st(p.refs_out + i, p.refs[i]);
+}
+
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
+    pages_compact_kernel(const Params p) {
+  __shared__ int red[33];
+  const int rank = cta_rank(), tid = threadIdx.x;
+  const int all = kCtas * kThreads, me = rank * kThreads + tid;
+  const int lane = tid & 31, wid = me >> 5, warps = all >> 5;
+  paged::grid_launch_dependents();
+
+  // 1. Live pages of each thread's share of the pool.
+  const int per = (p.P + all - 1) / all;
+  const int p0 = static_cast<int>(min(static_cast<long long>(p.P), static_cast<long long>(me) * per));
+  const int p1 = min(p.P, p0 + per);
+  int mine = 0, cta_total;
+  for (int i = p0; i < p1; ++i) mine += p.refs[i] > 0;
+  int at = block_scan(mine, red, &cta_total);
+  if (tid == 0) st(p.counts + rank, cta_total);
+  cluster_barrier();
+  int n = 0;
+  for (int r = 0; r < kCtas; ++r) {
+    const int c = ld(p.counts + r);
+    if (r < rank) at += c;
+    n += c;
+  }
+  // 2. The live pages before n; the others move. `at` counts the live pages
+  // before this share.
+  if (n == p.P) {
+    if (me == 0) st(p.n_copies, 0);
+  } else if (p0 <= n && n < p1) {
+    int before = at;
+    for (int i = p0; i < n; ++i) before += p.refs[i] > 0;
+    st(p.n_copies, n - before);
+  }
+  cluster_barrier();
+  const int moves = ld(p.n_copies), below = n - moves;  // live pages that stay
+  for (int i = p0; i < p1; ++i) {
+    const bool live = p.refs[i] > 0;
+    if (i < n && !live) st(p.to + (i - at), i);           // hole number i - (live before i)
+    if (i >= n && live) {
+      st(p.from + (at - below), i);
+      st(p.list + i, at - below);  // which move takes page i
+    }
+    if (live && i < n) st(p.refs_out + i, p.refs[i]);
+    if (i >= n) st(p.refs_out + i, 0);
+    at += live;
+  }
+  cluster_barrier();
+  // 3. Counts of the moved pages, and the tables.
+  for (int k = me; k < moves; k += all) st(p.refs_out + ld(p.to + k), p.refs[ld(p.from + k)]);
+  for (int b = wid; b < p.B; b += warps) {
+    const int len = p.lens[b], L = clamp_len(len, p), held = ceil_pages(L, p.page_log2);
+    if (lane == 0 && len > L) paged::bad(paged::kBadLength);
+    for (int j = lane; j < p.width; j += 32) {
+      const size_t e = static_cast<size_t>(b) * p.width + j;
+      int page = -1;
+      if (j < held) {
+        page = p.table[e];
+        if (page < 0 || page >= p.P || p.refs[page] <= 0)
+          paged::bad(paged::kBadPage);  // (left as it was)
+        else if (page >= n)
+          page = ld(p.to + ld(p.list + page));
+      }
+      p.table_out[e] = page;
+    }
+  }
+  if (me == 0) {
+    p.info[0] = n;
+    p.info[1] = moves;
+  }
+}
+
+// Contents of the pages from[k] into to[k], k < *n_copies, in every layer of
+// both pools. A page of a pool is `page_bytes` in one piece (a multiple of 16).
+struct CopyParams {
+  uint8_t* pool[2];
+  long long page_stride;   // bytes
+  long long layer_stride;  // bytes
+  long long page_bytes;
+  int layers;
+  const int* from;
+  const int* to;
+  const int* n_copies;
+};
+
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CopyParams p) {
+  paged::grid_wait();
+  const int n = *p.n_copies;
+  const int pieces = static_cast<int>((p.page_bytes + kCopyBytes - 1) / kCopyBytes);
+  const long long units = static_cast<long long>(n) * p.layers * 2 * pieces;
+  for (long long w = blockIdx.x; w < units; w += gridDim.x) {
+    const int piece = static_cast<int>(w % pieces);
+    const long long r = w / pieces;
+    const int layer = static_cast<int>((r >> 1) % p.layers);
+    const int k = static_cast<int>((r >> 1) / p.layers);
+    uint8_t* base = p.pool[r & 1] + layer * p.layer_stride;
+    const uint8_t* src = base + p.from[k] * p.page_stride;
+    uint8_t* dst = base + p.to[k] * p.page_stride;
+    const long long at = static_cast<long long>(piece) * kCopyBytes + threadIdx.x * 16;
+    uint4 v[kCopyUnroll];
+#pragma unroll
+    for (int i = 0; i < kCopyUnroll; ++i)
+      if (at + i * kCopyThreads * 16 < p.page_bytes)
+        v[i] = *reinterpret_cast<const uint4*>(src + at + i * kCopyThreads * 16);
+#pragma unroll
+    for (int i = 0; i < kCopyUnroll; ++i)
+      if (at + i * kCopyThreads * 16 < p.page_bytes)
+        *reinterpret_cast<uint4*>(dst + at + i * kCopyThreads * 16) = v[i];
+  }
+}
+
+}  // namespace pages
+}  // namespace eta

@@ -65,7 +65,9 @@ enum attn_status {
                                 B > 65,535; or the device is not sm_100 */
   ATTN_ERR_CUDA = -3,        /* a CUDA runtime call or launch failed */
   ATTN_ERR_TIMEOUT = -4,     /* a device-side wait gave up (see attn_get_device_status) */
-  ATTN_ERR_SCRATCH = -5      /* attn_decode_noalloc: sizes exceed its fixed scratch */
+  ATTN_ERR_SCRATCH = -5,     /* attn_decode_noalloc: sizes exceed its fixed scratch */
+  ATTN_ERR_PAGES = -6        /* bad page ids, lengths or rows in device memory (paged cache; see
+                                attn_get_device_status) */
 };
 
 /*
@@ -250,6 +252,197 @@ int attn_merge_partial_f16(float* o_acc, float* lse_acc, const float* o_part,
                            const float* lse_part, void* o_out, long long rows, int d,
                            attn_stream_t stream);
 
+/*
+ * Paged key/value cache.
+ *
+ * A pool holds num_pages pages of page_size tokens for Hkv KV heads; element
+ * (page, head, row, c) is at page * page_stride + head * head_stride +
+ * row * token_stride + c, in elements of the pool's type, the same in k and v.
+ * Both orders inside a page ([Hkv][page_size][d] and [page_size][Hkv][d]) and
+ * pools interleaved with others are described by the strides.
+ * Position t of sequence b lies in page table[b * table_width + t / page_size],
+ * row t % page_size.
+ *
+ * New tokens are packed: sequence b has T_b = cu_q[b + 1] - cu_q[b] of them,
+ * rows cu_q[b] .. cu_q[b + 1] of the packed tensors (cu_q: B + 1 entries, not
+ * decreasing), and kv_lens[b] = L_b cached tokens in all, the new ones
+ * included, so that its new token i is at position L_b - T_b + i. cu_q, kv_lens
+ * and the table are DEVICE memory, read only on the device.
+ *
+ * Sizes: d a multiple of 8 in [8, 256], page_size a power of two in [8, 1024]
+ * (others: ATTN_ERR_UNSUPPORTED), strides multiples of 8 elements and at least
+ * d, k and v 16-byte aligned, num_pages >= 1, table_width >= 1,
+ * table_width * page_size <= 2^30, at most 2^29 packed rows.
+ *
+ * Errors in device data cannot be refused on the host. They are never followed
+ * out of bounds: a page id outside [0, num_pages) where a sequence needs a
+ * page, lengths beyond the table, decreasing or overlong cu_q, a source row
+ * outside [-1, B) make attn_get_device_status() return ATTN_ERR_PAGES (raw code
+ * 0x2000 | what), and what the operators give for such a sequence is undefined.
+ */
+typedef struct attn_pages {
+  void* k;
+  void* v;
+  const int32_t* table;  /* [B][table_width], DEVICE memory */
+  long long page_stride; /* strides in elements */
+  long long head_stride;
+  long long token_stride;
+  int num_pages;
+  int page_size;
+  int table_width;
+  int Hkv;
+  int d;
+} attn_pages;
+
+/*
+ * Attention of new tokens over the paged cache: chunked prefill, decode (one
+ * new token per sequence) and any mix of the two in one batch. For new token i
+ * of sequence b, query head h and KV head g = h / (Hq / Hkv):
+ *     s_j = scale * q_i . k_j  for the keys j <= L_b - T_b + i, and, with
+ *           window >= 1, j > L_b - T_b + i - window
+ *     o_i = sum_j softmax_j(s) v_j,   lse_i = ln sum_j exp(s_j).
+ *   q    [total_q][Hq][d], rows of tokens q_stride elements apart (a multiple
+ *        of 8, >= Hq * d: q may be a part of a wider projection)
+ *   o    [total_q][Hq][d] contiguous     lse [total_q][Hq] float32, or NULL
+ *   max_q: no sequence has more new tokens than this.
+ *   window: 0 for none.
+ * The keys and values of the new tokens must be in the cache already
+ * (attn_rope_append puts them there). A token that sees no key gets o = 0,
+ * lse = -inf; rows of o and lse outside every sequence are left as they were.
+ * What pages hold behind L_b is not looked at, NaN and infinities included.
+ * Inside L_b they count as values: the value product runs over whole tiles of
+ * 128 keys, so an infinite or NaN v at a position that a token does not see
+ * may still reach it where other tokens see it (d <= 128).
+ * d <= 128 with at most 128 query heads per KV head runs on the tensor cores
+ * (any d below 64 or 128 at the cost of that size), other sizes on a CUDA-core
+ * kernel, far from the former's speed.
+ * Device memory: one workspace block from the library's pool, as attn_decode:
+ * on the tensor cores (B + 1) * 8 bytes, and per SM 16 bytes and
+ * 2 * 256 * (d + 1) * 4 bytes of partial results; else none.
+ */
+int attn_paged(const void* q, long long q_stride, const attn_pages* cache, const int32_t* cu_q,
+               const int32_t* kv_lens, void* o, float* lse, int B, int Hq, int total_q, int max_q,
+               float scale, int window, attn_stream_t stream);
+int attn_paged_f16(const void* q, long long q_stride, const attn_pages* cache, const int32_t* cu_q,
+                   const int32_t* kv_lens, void* o, float* lse, int B, int Hq, int total_q,
+                   int max_q, float scale, int window, attn_stream_t stream);
+
+/*
+ * Rotary positions. Pair p of a head's first rot values -- values p and
+ * p + rot / 2, or 2p and 2p + 1 when interleaved != 0 -- at position n is
+ * turned by a = 2 pi n turns[p]:
+ *     y_a = amp (x_a cos a - x_b sin a),   y_b = amp (x_b cos a + x_a sin a),
+ * and the other d - rot values pass through. backward != 0 gives the gradient
+ * of that map: q and k are then the gradients of its outputs (the angle is
+ * negated; values and gradients pass alike). The angle is formed in 64 bits,
+ * so far positions lose nothing; the rotation runs in fp32 and rounds once.
+ *   q, q_out [B, Hq, N, d] and k, k_out [B, Hkv, N, d], by strides in elements:
+ *        strides[0..2] batch, head, token of q, [3..5] of q_out, [6..8] of k,
+ *        [9..11] of k_out (HOST memory; multiples of 8; d contiguous). An
+ *        output may be its input (same pointer, same strides). Hq or Hkv may be 0.
+ *   pos  int32, DEVICE: pos[b * pos_stride + n] (pos_stride 0: shared)
+ *   turns [rot / 2] float64, DEVICE (attn_rope_turns computes them)
+ * Sizes: d a multiple of 8 in [8, 256], rot even in [0, d], Hq + Hkv <= 65,535,
+ * B * N < 2^31. rot a multiple of 16 runs with 16-byte accesses.
+ * Allocates nothing.
+ */
+int attn_rope(const void* q, void* q_out, const void* k, void* k_out, const long long* strides,
+              const int32_t* pos, long long pos_stride, const double* turns, int B, int Hq, int Hkv,
+              int N, int d, int rot, float amp, int interleaved, int backward,
+              attn_stream_t stream);
+int attn_rope_f16(const void* q, void* q_out, const void* k, void* k_out, const long long* strides,
+                  const int32_t* pos, long long pos_stride, const double* turns, int B, int Hq,
+                  int Hkv, int N, int d, int rot, float amp, int interleaved, int backward,
+                  attn_stream_t stream);
+
+/*
+ * Rotary positions of a serving step, fused with the append to the cache: the
+ * new tokens' q is rotated into q_out, k is rotated into the cache, v is copied
+ * into it.
+ *   q, q_out [total_q][Hq][d], k, v [total_q][Hkv][d], rows of tokens *_stride
+ *        elements apart (multiples of 8, at least a row); q_out may be q.
+ *   pos  [total_q] int32, DEVICE, or NULL: the tokens' positions in the cache.
+ * A token at a negative position (T_b > L_b) is not stored. rot = 0 appends
+ * without rotating. Pages that several sequences share must not be written:
+ * attn_pages_update gives each sequence that grows a last page of its own.
+ * Other arguments as in attn_paged and attn_rope. Allocates nothing.
+ */
+int attn_rope_append(const void* q, long long q_stride, void* q_out, long long q_out_stride,
+                     const void* k, long long k_stride, const void* v, long long v_stride,
+                     const attn_pages* cache, const int32_t* cu_q, const int32_t* kv_lens,
+                     const int32_t* pos, const double* turns, int B, int Hq, int total_q, int rot,
+                     float amp, int interleaved, attn_stream_t stream);
+int attn_rope_append_f16(const void* q, long long q_stride, void* q_out, long long q_out_stride,
+                         const void* k, long long k_stride, const void* v, long long v_stride,
+                         const attn_pages* cache, const int32_t* cu_q, const int32_t* kv_lens,
+                         const int32_t* pos, const double* turns, int B, int Hq, int total_q,
+                         int rot, float amp, int interleaved, attn_stream_t stream);
+
+/*
+ * Turns per position of each pair, f_p / 2 pi with f_p = base^(-2p / rot), and
+ * the amplitude (1 but for ATTN_ROPE_PARTS). HOST function, HOST memory:
+ * turns [rot / 2], amp [1]. rot even in [2, 256], base > 1. Scaling for contexts
+ * longer than the original one (factor >= 1):
+ *   ATTN_ROPE_LINEAR  f_p / factor
+ *   ATTN_ROPE_BASE    base * factor^(rot / (rot - 2)) in place of base (rot >= 4)
+ *   ATTN_ROPE_PARTS   pairs with more than `high` turns over `original`
+ *                     positions keep f_p, those with fewer than `low` get
+ *                     f_p / factor, with a ramp over the pairs between;
+ *                     amp = 0.1 ln(factor) + 1
+ *   ATTN_ROPE_BANDS   the same with the ramp over the number of turns:
+ *                     (original f_p / 2 pi - low) / (high - low); amp = 1
+ */
+enum attn_rope_scaling {
+  ATTN_ROPE_PLAIN = 0,
+  ATTN_ROPE_LINEAR = 1,
+  ATTN_ROPE_BASE = 2,
+  ATTN_ROPE_PARTS = 3,
+  ATTN_ROPE_BANDS = 4
+};
+int attn_rope_turns(double* turns, float* amp, int rot, double base, int scaling, double factor,
+                    double low, double high, double original);
+
+/*
+ * One step of the cache's bookkeeping: forks, beam steps, ended, new and
+ * growing sequences in one call. Row b of the next state goes on from row
+ * source[b] of this one (-1: from nothing) and grows by add[b] >= 0 tokens:
+ *   - rows that share a source share its full pages. Its last, partly filled
+ *     page stays with one of them, the source row itself if it goes on
+ *     (source[s] == s), else the first that takes it over; the others get a
+ *     copy of it, in all layers of both pools, in a page of their own;
+ *   - rows no longer taken over let go of their pages;
+ *   - a row gets fresh pages for the tokens that it grows by (their contents
+ *     are undefined). Free pages (refs <= 0 after the above) are taken lowest
+ *     first, in the order of the rows.
+ *   lens, refs, source, add: [B], [num_pages], [B], [B] int32; refs[p] counts
+ *        the rows that hold page p (and whoever else pins it). A row of L
+ *        tokens holds its first ceil(L / page_size) table entries.
+ *   table_out, lens_out, refs_out: the next state (entries behind a row's pages
+ *        are -1). They must not be the inputs.
+ *   info [2] int32: pages that were missing, and rows longer than the table
+ *        allows. If either is not 0 nothing has changed: the outputs are the
+ *        inputs, and no page was copied.
+ * All DEVICE memory. Values have 2 bytes; a page's Hkv * page_size * d values
+ * must lie in one piece (either order); layer l of the pools begins
+ * l * layer_stride elements behind k and v. Whole-number results do not depend
+ * on timing. One workspace block of (2 B + 3 max(B, num_pages)) * 4 bytes and a
+ * little more, as in attn_decode.
+ */
+int attn_pages_update(const attn_pages* cache, int layers, long long layer_stride,
+                      const int32_t* lens, const int32_t* refs, const int32_t* source,
+                      const int32_t* add, int32_t* table_out, int32_t* lens_out, int32_t* refs_out,
+                      int32_t* info, int B, attn_stream_t stream);
+
+/*
+ * Compaction: with n live pages (refs > 0), the live pages at n and above move,
+ * in order, into the free pages below n, in order -- the fewest copies -- in
+ * all layers of both pools; the tables and counts follow. info [2]: n, and the
+ * pages moved. Other arguments as in attn_pages_update.
+ */
+int attn_pages_compact(const attn_pages* cache, int layers, long long layer_stride,
+                       const int32_t* lens, const int32_t* refs, int32_t* table_out,
+                       int32_t* refs_out, int32_t* info, int B, attn_stream_t stream);
+
 /* Number of KV splits attn_decode uses for these sizes on the current device
    (>= 1; always 1 for d other than 64 and 128 and for the persistent pass of
    d = 128 with 2 to 32 query heads per KV head, which has no fixed split
@@ -266,8 +459,10 @@ const char* attn_strerror(int code);
 /*
  * Synchronises `stream`, then reads and clears the library's device status
  * word on the current device. Returns ATTN_OK, ATTN_ERR_TIMEOUT (a device
- * wait gave up; *raw_code, if not NULL, receives the site code) or
- * ATTN_ERR_CUDA.
+ * wait gave up), ATTN_ERR_PAGES (a paged-cache operator met bad device data) or
+ * ATTN_ERR_CUDA. *raw_code, if not NULL, receives the word: 0x1000 | site of
+ * the wait, or 0x2000 | what was bad (1 page id, 2 length, 3 rows, 4 source).
+ * The word holds the first error since it was last read.
  */
 int attn_get_device_status(attn_stream_t stream, unsigned int* raw_code);
 
