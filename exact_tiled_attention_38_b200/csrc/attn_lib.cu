@@ -535,10 +535,10 @@ int launch_decode_offsets(const int32_t* seqlens, long long* tok_off, int B, cud
 // Plan, persistent stream and gather of the d = 128 decode; `ws` holds the
 // layout `L`. seg_aligned: whole segments per CTA (L has no partials, and
 // there is nothing to gather).
-template <int NP, int GP, int HS, int D, typename T>
+template <int NP, int GP, int HS, int D, typename T, bool PAGED = false>
 int launch_decode_ps(const CUtensorMap& tq, decode_ps::PParams p, const PsLayout& L, char* ws,
-                     int nc, cudaStream_t st) {
-  auto kern = decode_ps::attn_decode_persistent_kernel<NP, GP, HS, D, T>;
+                     int nc, cudaStream_t st, const decode_ps::KvMaps<PAGED>& kv = {}) {
+  auto kern = decode_ps::attn_decode_persistent_kernel<NP, GP, HS, D, T, PAGED>;
   constexpr int smem = decode_ps::PCfg<NP, D>::kSmemBytes;
   static PerDeviceOnce attr;
   const cudaError_t attr_err = attr.run([&]() {
@@ -551,7 +551,7 @@ int launch_decode_ps(const CUtensorMap& tq, decode_ps::PParams p, const PsLayout
   p.part_o = L.part_o ? reinterpret_cast<float*>(ws + L.part_o) : nullptr;
   p.part_lse = L.part_lse ? reinterpret_cast<float*>(ws + L.part_lse) : nullptr;
   if (!p.inline_plan) {
-    decode_ps::attn_decode_plan_kernel<D><<<1, decode_ps::kPlanThreads, 0, st>>>(p, nc);
+    decode_ps::attn_decode_plan_kernel<D, PAGED><<<1, decode_ps::kPlanThreads, 0, st>>>(p, nc);
     const int rc = launch_status();
     if (rc != ATTN_OK) return rc;
   }
@@ -568,27 +568,29 @@ int launch_decode_ps(const CUtensorMap& tq, decode_ps::PParams p, const PsLayout
   cfg.stream = st;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tq, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tq, p, kv);
   if (e != cudaSuccess) return cuda_fail(e);
   if (p.seg_aligned) return launch_status();  // no cut segments, nothing to gather
-  const long long rows = static_cast<long long>(p.B) * p.Hq;
+  const long long rows = static_cast<long long>(p.B) * (PAGED ? p.Hkv * p.R : p.Hq);
   cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, decode_ps::attn_decode_gather_kernel<D, T>, p, nc);
+  e = cudaLaunchKernelEx(&cfg, decode_ps::attn_decode_gather_kernel<D, T, PAGED>, p, nc);
   if (e != cudaSuccess) return cuda_fail(e);
   return launch_status();
 }
 
-template <int D, typename T>
+template <int D, typename T, bool PAGED = false>
 int launch_decode_ps_group(const CUtensorMap& tq, const decode_ps::PParams& p, const PsLayout& L,
-                           char* ws, int nc, cudaStream_t st) {
-  if (p.G <= 4) return launch_decode_ps<16, 4, 1, D, T>(tq, p, L, ws, nc, st);
-  if (p.G <= 8) return launch_decode_ps<16, 8, 1, D, T>(tq, p, L, ws, nc, st);
-  if (p.G <= 16)
-    return launch_decode_ps<16, 16, D == 64 ? ETA_DECODE_PS_HS16_D64 : ETA_DECODE_PS_HS16_D128, D, T>(
-        tq, p, L, ws, nc, st);
-  return launch_decode_ps<32, 32, ETA_DECODE_PS_HS32, D, T>(tq, p, L, ws, nc, st);
+                           char* ws, int nc, cudaStream_t st,
+                           const decode_ps::KvMaps<PAGED>& kv = {}) {
+  const int rows = PAGED ? p.R : p.G;
+  if (rows <= 4) return launch_decode_ps<16, 4, 1, D, T, PAGED>(tq, p, L, ws, nc, st, kv);
+  if (rows <= 8) return launch_decode_ps<16, 8, 1, D, T, PAGED>(tq, p, L, ws, nc, st, kv);
+  if (rows <= 16)
+    return launch_decode_ps<16, 16, D == 64 ? ETA_DECODE_PS_HS16_D64 : ETA_DECODE_PS_HS16_D128, D, T,
+                            PAGED>(tq, p, L, ws, nc, st, kv);
+  return launch_decode_ps<32, 32, ETA_DECODE_PS_HS32, D, T, PAGED>(tq, p, L, ws, nc, st, kv);
 }
 
 // Batches of up to this many sequences skip the plan kernel: each CTA of the
@@ -630,7 +632,7 @@ int decode_ps_run(const void* q, const void* kc, const void* vc, const int32_t* 
   const int rc = encode_3d(&tq, q, bf16, d, G, static_cast<long long>(B) * Hkv,
                            static_cast<unsigned>(NP));
   if (rc != ATTN_OK) return rc;
-  decode_ps::PParams p;
+  decode_ps::PParams p = {};
   p.q = q;
   p.kc = kc;
   p.vc = vc;

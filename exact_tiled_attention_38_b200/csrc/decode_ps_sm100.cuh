@@ -63,6 +63,7 @@
 
 #include "common.cuh"
 #include "decode_sm100.cuh"
+#include "paged_common.cuh"
 
 namespace eta {
 namespace decode_ps {
@@ -200,6 +201,20 @@ struct PParams {
                     // the CTAs take equal shares of that cost (0: equal shares of the tiles)
   float scale_log2;
   uint64_t wait_ns;
+  // Paged cache (the kernels' PAGED form): a segment's rows are its sequence's
+  // new tokens times the group, R = max_q G of them at most.
+  int R;            // rows of a partial slot (G for the packed cache)
+  const int* cu_q;  // [B + 1]
+  paged::Cache cache;
+  int total_q, max_q;
+};
+
+// Tensor maps of the pools, of the PAGED form only.
+template <bool PAGED>
+struct KvMaps {};
+template <>
+struct KvMaps<true> {
+  CUtensorMap k, v;
 };
 
 // Programmatic dependent launch: a grid launched with programmatic stream
@@ -216,16 +231,62 @@ __device__ __forceinline__ int first_key(int len, int window) {
   return (window > 0 && len > window) ? len - window : 0;
 }
 
+// Length, rows and first key of sequence b. PAGED: T new tokens at rows q0 on,
+// the first of which sees back to key k0; without new tokens nothing is read.
+struct SeqKeys {
+  int len, k0, nt, q0, T;
+};
+template <bool PAGED>
+__device__ __forceinline__ SeqKeys seq_keys(const PParams& p, int b) {
+  SeqKeys s;
+  if constexpr (PAGED) {
+    const paged::Seq q =
+        paged::load_seq(p.cu_q, p.seqlens, b, p.total_q, p.max_q, p.cache.capacity());
+    s.q0 = q.q0;
+    s.T = q.T;
+    s.len = q.T > 0 ? q.L : 0;
+    // (tiles begin where the cache's do, so that whole pages fall into a tile)
+    s.k0 = p.window > 0 ? min(max(0, q.L - q.T - p.window + 1), max(s.len - 1, 0)) & ~(TK - 1) : 0;
+  } else {
+    s.q0 = 0;
+    s.T = 1;
+    s.len = max(p.seqlens[b], 0);
+    s.k0 = first_key(s.len, p.window);
+  }
+  s.nt = (s.len - s.k0 + TK - 1) / TK;
+  return s;
+}
+
+// O = 0, LSE = -inf for the rows of a sequence without keys.
+template <int D, bool PAGED>
+__device__ __forceinline__ void write_empty(const PParams& p, int b) {
+  if constexpr (PAGED) {
+    const SeqKeys s = seq_keys<true>(p, b);
+    for (long long h = 0; h < static_cast<long long>(s.T) * p.Hq; ++h) {
+      const size_t row = static_cast<size_t>(s.q0) * p.Hq + h;
+      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.o) + row * p.cache.d);
+      for (int u = 0; u < p.cache.d / 8; ++u) dst[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse != nullptr) p.lse[row] = -INFINITY;
+    }
+  } else {
+    for (int h = 0; h < p.Hq; ++h) {
+      const size_t row = static_cast<size_t>(b) * p.Hq + h;
+      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.o) + row * D);
+      for (int u = 0; u < D / 8; ++u) dst[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse != nullptr) p.lse[row] = -INFINITY;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ plan
 // Exclusive prefix sums over the B sequences (one CTA): token offsets of the
 // packed cache and tile offsets of the global tile order (Hkv segments of
 // ceil(keys read / 128) tiles per sequence). tile_off[B] is the total.
-template <int D>
+template <int D, bool PAGED = false>
 __global__ void __launch_bounds__(kPlanThreads) attn_decode_plan_kernel(const PParams p, int nc) {
-  const int* __restrict__ seqlens = p.seqlens;
   long long* __restrict__ tok_off = const_cast<long long*>(p.tok_off);
   int* __restrict__ tile_off = const_cast<int*>(p.tile_off);
-  const int B = p.B, Hkv = p.Hkv, window = p.window;
+  const int B = p.B, Hkv = p.Hkv;
   __shared__ long long s_tok[kPlanThreads / 32];
   __shared__ long long s_til[kPlanThreads / 32];
   griddep_launch_dependents();  // the stream kernel may start its set-up now
@@ -234,9 +295,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_decode_plan_kernel(const PP
   const int b1 = min(B, b0 + per);
   long long tok = 0, til = 0;
   for (int b = b0; b < b1; ++b) {
-    const int len = max(seqlens[b], 0);
-    tok += len;
-    til += static_cast<long long>(Hkv) * ((len - first_key(len, window) + TK - 1) / TK);
+    const SeqKeys s = seq_keys<PAGED>(p, b);
+    if constexpr (PAGED)
+      paged::check_seq(p.cu_q, p.seqlens, b, p.total_q, p.max_q, p.cache.capacity());
+    tok += s.len;
+    til += static_cast<long long>(Hkv) * s.nt;
   }
   // inclusive scan over the block: warps, then warp totals
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -274,18 +337,12 @@ __global__ void __launch_bounds__(kPlanThreads) attn_decode_plan_kernel(const PP
   long long l_run = xl - til + (warp > 0 ? s_til[warp - 1] : 0);
   const long long T = s_til[31];  // all tiles
   for (int b = b0; b < b1; ++b) {
-    const int len = max(seqlens[b], 0);
-    const int nt = (len - first_key(len, window) + TK - 1) / TK;
+    const SeqKeys s = seq_keys<PAGED>(p, b);
+    const int len = s.len, nt = s.nt;
     tok_off[b] = t_run;
     tile_off[b] = static_cast<int>(l_run);
     if (nt == 0) {
-      // An empty sequence: no CTA visits it. O = 0, LSE = -inf.
-      for (int h = 0; h < p.Hq; ++h) {
-        const size_t row = static_cast<size_t>(b) * p.Hq + h;
-        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.o) + row * D);
-        for (int u = 0; u < D / 8; ++u) dst[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (p.lse != nullptr) p.lse[row] = -INFINITY;
-      }
+      write_empty<D, PAGED>(p, b);  // no CTA visits it
     } else if (!p.seg_aligned) {
       // CTAs of the equal tile ranges whose first tile lies in this sequence:
       // CTA c starts at tile c * T / nc.
@@ -345,16 +402,21 @@ __host__ __device__ __forceinline__ int cta_of(long long t, long long T, int nc)
 }
 
 // Position of a global tile: sequence b, KV head g, tile i of nt in the segment.
+template <bool PAGED>
 struct Cursor {
   int b, g, i, nt;
   int len, k0;        // keys read of sequence b: [k0, len)
+  int q0, T;          // PAGED: its new tokens
   long long tok;      // token offset of sequence b
 
   // Length, first key and tile count of sequence b (tok is kept by the caller).
   __device__ __forceinline__ void load_seq(const PParams& p) {
-    len = max(p.seqlens[b], 0);
-    k0 = first_key(len, p.window);
-    nt = (len - k0 + TK - 1) / TK;
+    const SeqKeys s = seq_keys<PAGED>(p, b);
+    len = s.len;
+    k0 = s.k0;
+    nt = s.nt;
+    q0 = s.q0;
+    T = s.T;
   }
   __device__ __forceinline__ void seek(const PParams& p, long long t) {
     int lo = 0, hi = p.B - 1;  // largest b with tile_off[b] <= t
@@ -518,9 +580,15 @@ __device__ __forceinline__ void gather4(const float* red, float (&out)[GP], Op o
 // NP: MMA width (the group padded to 16 or 32); GP <= NP: the heads the
 // softmax processes (the group padded to 4, 8, 16 or 32); HS: softmax warps
 // per key quarter (1, 2 or 4), each taking GP / HS >= 4 of the heads.
-template <int NP, int GP, int HS, int D, typename T>
+// PAGED: the cache is paged and a sequence may have several new tokens; "head"
+// then stands for a row (new token, head of the group), token by token, of
+// which there are T G <= GP, each with the keys up to its own position. Head
+// sizes below D are padded with zeros as they are loaded.
+template <int NP, int GP, int HS, int D, typename T, bool PAGED = false>
 __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
-    attn_decode_persistent_kernel(const __grid_constant__ CUtensorMap tm_q, const PParams p) {
+    attn_decode_persistent_kernel(const __grid_constant__ CUtensorMap tm_q, const PParams p,
+                                  const __grid_constant__ KvMaps<PAGED> tm_kv) {
+  static_assert(!PAGED || ETA_DECODE_PS_KV_SPLIT, "K and V of a tile on their own barriers");
   static_assert(GP == 4 || GP == 8 || GP == 16 || GP == 32, "softmax group");
   static_assert(GP <= NP && (GP > 16) == (NP == 32), "widths");
   static_assert((HS == 1 || HS == 2 || HS == 4) && GP % HS == 0 && GP / HS >= 4, "head split");
@@ -567,9 +635,9 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
 
   if (threadIdx.x == 32) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 32);  // one cp.async arrival per producer lane
+      mbar_init(&full[s], PAGED ? 1 : 32);  // one cp.async arrival per producer lane, or one TMA count
       mbar_init(&empty[s], 1);
-      mbar_init(&full_v[s], 32);
+      mbar_init(&full_v[s], PAGED ? 1 : 32);
       mbar_init(&empty_v[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -618,7 +686,7 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
   Range rg;
-  Cursor cur;
+  Cursor<PAGED> cur;
   if (p.inline_plan) {
     // Prefix sums over the sequences in this CTA (small batches): the total
     // tile count, this CTA's range and its first tile, without a plan kernel.
@@ -642,8 +710,10 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
     const int w = p.wcost;
     long long til = 0, tok = 0;
     for (int b = b0; b < b1; ++b) {
-      const int len = max(p.seqlens[b], 0);
-      const int nt = (len - first_key(len, p.window) + TK - 1) / TK;
+      const SeqKeys sk = seq_keys<PAGED>(p, b);
+      const int len = sk.len, nt = sk.nt;
+      if constexpr (PAGED)
+        if (c == 0) paged::check_seq(p.cu_q, p.seqlens, b, p.total_q, p.max_q, p.cache.capacity());
       tok += len + (nt > 0 ? kSeqOne : 0);
       til += static_cast<long long>(p.Hkv) * nt;
     }
@@ -694,19 +764,12 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
     const long long x_lo = div_nonneg(c * C_all, gridDim.x);
     const long long x_hi = div_nonneg((c + 1) * C_all, gridDim.x);
     for (int b = b0; b < b1; ++b) {
-      const int len = max(p.seqlens[b], 0);
-      const int nt = (len - first_key(len, p.window) + TK - 1) / TK;
+      const SeqKeys sk = seq_keys<PAGED>(p, b);
+      const int len = sk.len, nt = sk.nt;
       const long long span = static_cast<long long>(p.Hkv) * nt;
       const long long kspan = nt > 0 ? span + wseg : 0;
       if (c == 0) const_cast<int*>(p.tile_off)[b] = static_cast<int>(k_run);
-      if (nt == 0 && b % static_cast<int>(gridDim.x) == c) {
-        for (int h = 0; h < p.Hq; ++h) {
-          const size_t row = static_cast<size_t>(b) * p.Hq + h;
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.o) + row * D);
-          for (int u = 0; u < D / 8; ++u) dst[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (p.lse != nullptr) p.lse[row] = -INFINITY;
-        }
-      }
+      if (nt == 0 && b % static_cast<int>(gridDim.x) == c) write_empty<D, PAGED>(p, b);
       // The tile at or after cost position x of this sequence, as its rank
       // g nt + i among the sequence's tiles (segment g, tile i; one of a
       // segment's wcost leading positions gives its first tile). Segments
@@ -778,21 +841,60 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
     const uint32_t kdst = smem_u32(smem + pw * C::kStageBytes);
     const uint32_t vdst = kdst + C::kTileBytes;
     const int u = lane % UPR;
+    [[maybe_unused]] const int box_rows = PAGED ? min(1 << p.cache.page_log2, TK) : TK;
+    [[maybe_unused]] const int lanes = TK / box_rows * C::kBoxes;
+    [[maybe_unused]] int nk = 0, nv = 0;  // PAGED: tiles issued into this stage
     for (int a = 0; a < pw && a + 1 < n; ++a) cur.next(p);  // to tile pw (if in range)
     for (int j = pw; ok && j < n; j += kStages) {
       const int use = j / kStages;
+      // PAGED: lane l copies page l / boxes of the tile, 64 columns of it, by
+      // one TMA load; its page id is read while the stage is still in use.
+      // What the sequence does not have (pages behind its last, or an id
+      // outside the pool) is loaded out of range: zeros, nothing is read.
+      [[maybe_unused]] int page = 0;
+      if constexpr (PAGED) {
+        const int key = cur.k0 + cur.i * TK + (lane / C::kBoxes) * box_rows;
+        page = p.cache.num_pages;
+        if (lane < lanes && key < cur.len) {
+          const int id = p.cache.table[static_cast<size_t>(cur.b) * p.cache.width +
+                                       (key >> p.cache.page_log2)];
+          if (id >= 0 && id < p.cache.num_pages)
+            page = id;
+          else
+            paged::bad(paged::kBadPage);
+        }
+      }
       if (use > 0 &&
           !(ok = decode::warp_all_d(wait_bar_spin(&empty[pw], (use - 1) & 1, ctl, kSiteEmpty))))
         break;
       if (ETA_DECODE_PS_STAGGER && use == 0 && pw > 0 &&
           !(ok = decode::warp_all_d(wait_bar_spin(&first_issued[pw - 1], 0, ctl, kSiteEmpty))))
         break;  // the first stages go out in order, so the first tile lands first
+      const int t0 = cur.k0 + cur.i * TK;
       const size_t head_base =
           (static_cast<size_t>(cur.tok) * p.Hkv + static_cast<size_t>(cur.g) * cur.len) * D;
       const T* kbase = reinterpret_cast<const T*>(p.kc) + head_base;
       const T* vbase = reinterpret_cast<const T*>(p.vc) + head_base;
-      const int t0 = cur.k0 + cur.i * TK;
-      if constexpr (ETA_DECODE_PS_KV_SPLIT) {
+      if constexpr (PAGED) {
+        // K on its own barrier and then V, as below.
+        const uint32_t off = (lane % C::kBoxes) * C::kBoxBytes + (lane / C::kBoxes) * box_rows * 128;
+        const int y = (t0 + (lane / C::kBoxes) * box_rows) & ((1 << p.cache.page_log2) - 1);
+        uint8_t* stage = smem + pw * C::kStageBytes;
+        if (lane == 0) mbar_arrive_expect_tx(&full[pw], C::kTileBytes);
+        __syncwarp();
+        if (lane < lanes)
+          paged::tma_load_4d(stage + off, &tm_kv.k, &full[pw], (lane % C::kBoxes) * 64, y, cur.g, page);
+        ++nk;
+        if (use > 0 &&
+            !(ok = decode::warp_all_d(wait_bar_spin(&empty_v[pw], (use - 1) & 1, ctl, kSiteEmpty))))
+          break;
+        if (lane == 0) mbar_arrive_expect_tx(&full_v[pw], C::kTileBytes);
+        __syncwarp();
+        if (lane < lanes)
+          paged::tma_load_4d(stage + C::kTileBytes + off, &tm_kv.v, &full_v[pw],
+                             (lane % C::kBoxes) * 64, y, cur.g, page);
+        ++nv;
+      } else if constexpr (ETA_DECODE_PS_KV_SPLIT) {
         // K, then (once PV(j - 3) has read the stage's V tile) V; each
         // arrival fires when all this lane's earlier copies have landed.
 #pragma unroll 4
@@ -836,7 +938,13 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
       }
       for (int a = 0; a < kStages && j + 1 + a < n; ++a) cur.next(p);
     }
-    cp_async_wait_all();  // no copy may land after the CTA exits
+    // No copy may land after the CTA exits.
+    if constexpr (PAGED) {
+      if (nk > 0) drain_bar(&full[pw], (nk - 1) & 1, ctl, kSiteDrain);
+      if (nv > 0) drain_bar(&full_v[pw], (nv - 1) & 1, ctl, kSiteDrain);
+    } else {
+      cp_async_wait_all();
+    }
   } else if (warp == R::kMma) {
     // ------------------------------------------------------------ MMA issue and Q loads
     constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
@@ -852,22 +960,31 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
     // Q of piece k goes to buffer k % 2 (its G rows; rows G..NP-1 are zero-filled
     // by the copy as out of bounds). The first piece's Q is loaded here.
     int nq0 = 0, nq1 = 0;  // Q loads issued per buffer (scalars: no local-memory array)
-    auto load_q = [&](int buf, int seg) {
+    auto load_q = [&](int buf, const Cursor<PAGED>& at) {
       if (buf)
         ++nq1;
       else
         ++nq0;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&q_full[buf], C::kQBuf);
-        for (int bx = 0; bx < C::kBoxes; ++bx)
-          tma_load_3d(sQ + buf * C::kQBuf + bx * C::kQBox, &tm_q, &q_full[buf], bx * 64, 0, seg);
+        if constexpr (PAGED) {  // rows (token, head) of max_q tokens; only the sequence's own count
+          mbar_arrive_expect_tx(&q_full[buf], static_cast<uint32_t>(C::kBoxes * p.R * 128));
+          for (int bx = 0; bx < C::kBoxes; ++bx)
+            paged::tma_load_4d(sQ + buf * C::kQBuf + bx * C::kQBox, &tm_q, &q_full[buf], bx * 64, 0,
+                               at.g, at.q0);
+        } else {
+          mbar_arrive_expect_tx(&q_full[buf], C::kQBuf);
+          for (int bx = 0; bx < C::kBoxes; ++bx)
+            tma_load_3d(sQ + buf * C::kQBuf + bx * C::kQBox, &tm_q, &q_full[buf], bx * 64, 0,
+                        at.segment(p));
+        }
       }
       __syncwarp();
     };
-    load_q(0, cur.segment(p));
+    load_q(0, cur);
     bool ok = true;
     int k = -1;                // current piece
     bool prev_first = false;   // tile j - 1 started its piece
+    [[maybe_unused]] int prev_keys = TK;  // PAGED: keys of tile j - 1
     uint32_t qb = 0;
     for (int j = 0; ok && j <= n; ++j) {
       if (j < n) {
@@ -904,12 +1021,12 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
         if (first && j + (cur.nt - cur.i) < n) {
           // Load the next piece's Q into the other buffer, which piece k - 1
           // used: wait until its last score product has read it.
-          Cursor nx = cur;  // first tile of the next piece, tile j + nt - i (< n)
+          Cursor<PAGED> nx = cur;  // first tile of the next piece, tile j + nt - i (< n)
           for (int a = cur.i; a < cur.nt; ++a) nx.next(p);
           if (k >= 1 && !(ok = decode::warp_all_d(
                               wait_bar_spin(&q_free[qb ^ 1], ((k - 1) >> 1) & 1, ctl, kSiteQFree))))
             break;
-          load_q(qb ^ 1, nx.segment(p));
+          load_q(qb ^ 1, nx);
         }
       }
       if (j >= 1) {
@@ -922,7 +1039,21 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
             !(ok = decode::warp_all_d(
                   wait_bar_spin(&full_v[st], (jp / kStages) & 1, ctl, kSiteFull))))
           break;
+        if constexpr (PAGED) {
+          // Rows of V behind the sequence's last key: zeros, whatever lies in
+          // the pool there (their probabilities are zero, but 0 * NaN is not).
+          if (prev_keys < TK) {
+            uint8_t* vt = smem + st * C::kStageBytes + C::kTileBytes;
+            for (int i = lane; i < (TK - prev_keys) * C::kBoxes * 8; i += 32) {
+              const int row = prev_keys + (i >> 3) / C::kBoxes, box = (i >> 3) % C::kBoxes;
+              *reinterpret_cast<uint4*>(vt + box * C::kBoxBytes + row * 128 + (i & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            __syncwarp();
+          }
+        }
         fence_proxy_async_smem();
+        if constexpr (PAGED) __syncwarp();
         tc_fence_after();
         const uint32_t vd = v_lo + ((st * C::kStageBytes) >> 4);
         const uint32_t pd = p_lo + (((jp & 1) * C::kPBuf) >> 4);
@@ -940,6 +1071,7 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
       }
       if (j < n) {
         prev_first = (j == 0) || (cur.i == 0);
+        if constexpr (PAGED) prev_keys = cur.len - (cur.k0 + cur.i * TK);
         if (j + 1 < n) cur.next(p);
       }
     }
@@ -972,6 +1104,11 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
       fence_proxy_async_smem();
     }
     float m[GPT], l[GPT];
+    // PAGED: the last key that each of this thread's rows sees (-1: no row),
+    // and how many keys back it sees.
+    [[maybe_unused]] int last_key[GPT];
+    [[maybe_unused]] const unsigned reach = p.window > 0 ? static_cast<unsigned>(p.window) : 0x80000000u;
+    int rows = G;  // rows of the current segment
     bool ok = true;
     uint32_t xc = 0;        // uses of the x_bar / red exchange so far
     bool piece_whole = false;
@@ -985,6 +1122,12 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
           m[h] = -INFINITY;
           l[h] = 0.f;
         }
+        if constexpr (PAGED) {
+          rows = cur.T * G;
+#pragma unroll
+          for (int h = 0; h < GPT; ++h)
+            last_key[h] = h0 + h < rows ? cur.len - cur.T + (h0 + h) / G : -1;
+        }
       }
       if (last) piece_whole = piece_whole && (cur.i == cur.nt - 1);
       if (!(ok = decode::warp_all_d(wait_bar_spin(&s_ready[j & 1], (j >> 1) & 1, ctl, kSiteS)))) break;
@@ -995,7 +1138,12 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
       float s[GPT], wm[GPT];
 #pragma unroll
       for (int h = 0; h < GPT; ++h) {
-        s[h] = (valid && h0 + h < G) ? __uint_as_float(r[h]) * sl2 : -INFINITY;
+        bool sees;
+        if constexpr (PAGED)
+          sees = static_cast<unsigned>(last_key[h] - (cur.k0 + cur.i * TK + krow)) < reach;
+        else
+          sees = valid && h0 + h < G;
+        s[h] = sees ? __uint_as_float(r[h]) * sl2 : -INFINITY;
         wm[h] = s[h];
       }
       float* rb = red + (xc & 1) * (kSoftWarps * NP);
@@ -1083,7 +1231,7 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
 #pragma unroll
       for (int h = 0; h < GPT; ++h) {
         float pv = 0.f;
-        if (h0 + h < G) {
+        if (h0 + h < rows) {
           pv = ex2_approx(s[h] - (m[h] == -INFINITY ? 0.f : m[h]));
           l[h] += pv;
         }
@@ -1119,17 +1267,25 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
 #pragma unroll
         for (int h = 0; h < GPT; ++h) {
           const int hg = h0 + h;
-          if (hg < G && dim < D) {
+          if (hg < rows && dim < (PAGED ? p.cache.d : D)) {
             const float ov = tot[h] > 0.f ? __uint_as_float(o[h]) / tot[h] : 0.f;
             const float l2 = tot[h] > 0.f ? m[h] + lg2_approx(tot[h]) : -INFINITY;
             if (piece_whole) {
               // The whole segment lay in this CTA: this is the result.
-              reinterpret_cast<uint16_t*>(p.o)[(row0 + hg) * D + dim] = to_bits<T>(ov);
-              if (dim == hg && p.lse != nullptr) p.lse[row0 + hg] = l2 * 0.69314718055994531f;
+              if constexpr (PAGED) {
+                const int tok = hg / G;
+                const size_t row = (static_cast<size_t>(cur.q0) + tok) * p.Hq + cur.g * G + hg - tok * G;
+                reinterpret_cast<uint16_t*>(p.o)[row * p.cache.d + dim] = to_bits<T>(ov);
+                if (dim == 0 && p.lse != nullptr) p.lse[row] = l2 * 0.69314718055994531f;
+              } else {
+                reinterpret_cast<uint16_t*>(p.o)[(row0 + hg) * D + dim] = to_bits<T>(ov);
+                if (dim == hg && p.lse != nullptr) p.lse[row0 + hg] = l2 * 0.69314718055994531f;
+              }
             } else {
               const size_t slot = static_cast<size_t>(seg) + c;
-              p.part_o[(slot * G + hg) * D + dim] = ov;
-              if (dim == hg) p.part_lse[slot * G + hg] = l2;
+              const int R = PAGED ? p.R : G;
+              p.part_o[(slot * R + hg) * D + dim] = ov;
+              if (dim == (PAGED ? 0 : hg)) p.part_lse[slot * R + hg] = l2;
             }
           }
         }
@@ -1155,17 +1311,21 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
 // equal-tile-range mode) has one partial per CTA, in slots segment + cta;
 // merge them by their log-sum-exp. Segments that lay in one CTA were written
 // by it, and empty sequences by the plan kernel; both are skipped.
-template <int D, typename T>
+// PAGED: one warp per (sequence, KV head, row of its R), the rows being (new
+// token, head of the group).
+template <int D, typename T, bool PAGED = false>
 __global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p, int nc) {
   constexpr int EPL = D / 32;  // output elements per lane
   griddep_wait();  // the stream kernel's partials and outputs are visible after this
   const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  if (row >= static_cast<long long>(p.B) * p.Hq) return;
-  const int b = static_cast<int>(div_nonneg(row, p.Hq));
-  const int h = static_cast<int>(row - static_cast<long long>(b) * p.Hq);
-  const int g = h / p.G;
-  const int hh = h - g * p.G;
+  const int R = PAGED ? p.R : p.G;         // rows of a segment's slot
+  const int per_seq = PAGED ? p.Hkv * R : p.Hq;
+  if (row >= static_cast<long long>(p.B) * per_seq) return;
+  const int b = static_cast<int>(div_nonneg(row, per_seq));
+  const int h = static_cast<int>(row - static_cast<long long>(b) * per_seq);
+  const int g = h / R;
+  const int hh = h - g * R;
   // tile_off holds cost positions (tile offsets when wcost = 0): a non-empty
   // sequence spans Hkv (nt + wcost) of them, and tile i of its segment g sits
   // at tile_off[b] + g (nt + wcost) + wcost + i.
@@ -1195,7 +1355,7 @@ __global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p
     const int cc = c0 + k;
     lse_r[k] = -INFINITY;
     if (cc <= c1 && has_tiles(cc)) {
-      const long long slot = (seg + cc) * p.G + hh;
+      const long long slot = (seg + cc) * R + hh;
       lse_r[k] = p.part_lse[slot];
       const float* x = p.part_o + slot * D + lane * EPL;
       if constexpr (EPL == 4) {
@@ -1226,7 +1386,7 @@ __global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p
   for (int k = 0; k < kMaxP; ++k) fold(lse_r[k], xv[k]);
   for (int cc = c0 + kMaxP; cc <= c1; ++cc) {
     if (!has_tiles(cc)) continue;
-    const long long slot = (seg + cc) * p.G + hh;
+    const long long slot = (seg + cc) * R + hh;
     const float* x = p.part_o + slot * D + lane * EPL;
     float xr[EPL];
 #pragma unroll
@@ -1234,16 +1394,26 @@ __global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p
     fold(p.part_lse[slot], xr);
   }
   const float inv = tot > 0.f ? 1.f / tot : 0.f;
+  long long orow = row;
+  int cols = D;
+  if constexpr (PAGED) {
+    const SeqKeys sk = seq_keys<true>(p, b);
+    if (hh >= sk.T * p.G) return;  // no such row: its slot was not written
+    const int tok = hh / p.G;
+    orow = (static_cast<long long>(sk.q0) + tok) * p.Hq + g * p.G + hh - tok * p.G;
+    cols = p.cache.d;
+    if (lane * EPL >= cols) return;  // (lane 0 stays)
+  }
   uint32_t pk[EPL / 2];
 #pragma unroll
   for (int e = 0; e < EPL / 2; ++e) pk[e] = decode::pack2<T>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  T* dst = reinterpret_cast<T*>(p.o) + row * D + lane * EPL;
+  T* dst = reinterpret_cast<T*>(p.o) + orow * cols + lane * EPL;
   if constexpr (EPL == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
   else
     *reinterpret_cast<uint32_t*>(dst) = pk[0];
   if (lane == 0 && p.lse != nullptr)
-    p.lse[row] = tot > 0.f ? (mx + lg2_approx(tot)) * 0.69314718055994531f : -INFINITY;
+    p.lse[orow] = tot > 0.f ? (mx + lg2_approx(tot)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace decode_ps

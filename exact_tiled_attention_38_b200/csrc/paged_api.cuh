@@ -100,6 +100,30 @@ struct Workspace {
   }
 };
 
+// Maps of the pools, boxes of 64 columns and one page (or 128 rows of it).
+inline int encode_pools(CUtensorMap* tk, CUtensorMap* tv, const paged::Cache& c, bool bf16) {
+  const int page = 1 << c.page_log2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(page),
+                              static_cast<cuuint64_t>(c.Hkv), static_cast<cuuint64_t>(c.num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.token_stride) * 2,
+                                 static_cast<cuuint64_t>(c.head_stride) * 2,
+                                 static_cast<cuuint64_t>(c.page_stride) * 2};
+  const unsigned rows = static_cast<unsigned>(page < paged::BN ? page : paged::BN);
+  const int rc = encode_4d(tk, c.k, bf16, dims, strides, rows, 1);
+  return rc != ATTN_OK ? rc : encode_4d(tv, c.v, bf16, dims, strides, rows, 1);
+}
+
+// Map of the packed queries, boxes of 64 columns, a group's heads, `tokens` tokens.
+inline int encode_queries(CUtensorMap* tq, const void* q, long long q_stride, const paged::Cache& c,
+                          int G, int total_q, int tokens, bool bf16) {
+  const cuuint64_t d = static_cast<cuuint64_t>(c.d);
+  const cuuint64_t dims[4] = {d, static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(c.Hkv),
+                              static_cast<cuuint64_t>(total_q)};
+  const cuuint64_t strides[3] = {d * 2, d * 2 * G, static_cast<cuuint64_t>(q_stride) * 2};
+  return encode_4d(tq, q, bf16, dims, strides, static_cast<unsigned>(G),
+                   static_cast<unsigned>(tokens));
+}
+
 template <int D, typename T>
 int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                  const paged::Params& p, cudaStream_t st) {
@@ -119,6 +143,53 @@ int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap
     rc = launch_dependent(paged::attn_paged_gather_kernel<T>,
                           dim3(static_cast<unsigned>(p.nc), 4), 256, 0, st, p);
   return rc;
+}
+
+// Few rows of a KV head (max_q G <= 32): the persistent decode pass, whose
+// products have the keys on the tensor core's long side, over pages. Batches whose
+// tiles could not be counted in 32 bits take the other kernel.
+template <typename T>
+int paged_decode_run(const void* q, long long q_stride, const paged::Cache& c, const int32_t* cu_q,
+                     const int32_t* kv_lens, void* o, float* lse, int B, int Hq, int total_q,
+                     int max_q, float scale, int window, int nc, cudaStream_t st) {
+  constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  const int G = Hq / c.Hkv, D = c.d <= 64 ? 64 : 128;
+  decode_ps::PParams p = {};
+  p.q = q;
+  p.kc = c.k;
+  p.vc = c.v;
+  p.seqlens = kv_lens;
+  p.o = o;
+  p.lse = lse;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = c.Hkv;
+  p.G = G;
+  p.window = window;
+  p.inline_plan = B <= ETA_DECODE_INLINE_PLAN_MAX_B ? 1 : 0;
+  p.R = max_q * G;
+  p.wcost = !p.inline_plan ? 0
+            : p.R <= 8     ? 0
+            : p.R <= 16    ? ETA_DECODE_PS_SEG_COST16
+                           : ETA_DECODE_PS_SEG_COST32;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.wait_ns = kDefaultWaitNs;
+  p.cu_q = cu_q;
+  p.cache = c;
+  p.total_q = total_q;
+  p.max_q = max_q;
+  CUtensorMap tq;
+  decode_ps::KvMaps<true> kv;
+  int rc = encode_queries(&tq, q, q_stride, c, G, total_q, max_q, bf16);
+  if (rc == ATTN_OK) rc = encode_pools(&kv.k, &kv.v, c, bf16);
+  if (rc != ATTN_OK) return rc;
+  const PsLayout L = ps_layout(B, c.Hkv, p.R, D, nc, true);
+  Workspace ws;
+  rc = ws.take(L.total, st);
+  if (rc != ATTN_OK) return rc;
+  rc = D == 128 ? launch_decode_ps_group<128, T, true>(tq, p, L, static_cast<char*>(ws.p), nc, st, kv)
+                : launch_decode_ps_group<64, T, true>(tq, p, L, static_cast<char*>(ws.p), nc, st, kv);
+  return ws.give_back(rc);
 }
 
 template <typename T>
@@ -172,22 +243,18 @@ int paged_run(const void* q, long long q_stride, const attn_pages* pages, const 
     return launch_status();
   }
 
+  // (the global tile order and the gather's rows are counted in 32 bits)
+  const long long tiles = static_cast<long long>(B) * c.Hkv * ((c.capacity() >> 7) + 4);
+  if (static_cast<long long>(max_q) * G <= 32 && tiles < 0x7fffffffLL &&
+      static_cast<long long>(B) * c.Hkv * max_q * G < (1ll << 32))
+    return paged_decode_run<T>(q, q_stride, c, cu_q, kv_lens, o, lse, B, Hq, total_q, max_q, scale,
+                               window, info.sm_count, st);
+
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   const int tt = paged::BM / G;
-  const cuuint64_t d = static_cast<cuuint64_t>(c.d);
-  const unsigned box_rows = static_cast<unsigned>(pages->page_size < paged::BN ? pages->page_size : paged::BN);
-  const cuuint64_t qd[4] = {d, static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(c.Hkv),
-                            static_cast<cuuint64_t>(total_q)};
-  const cuuint64_t qs[3] = {d * 2, d * 2 * G, static_cast<cuuint64_t>(q_stride) * 2};
-  const cuuint64_t kd[4] = {d, static_cast<cuuint64_t>(pages->page_size),
-                            static_cast<cuuint64_t>(c.Hkv), static_cast<cuuint64_t>(c.num_pages)};
-  const cuuint64_t ks[3] = {static_cast<cuuint64_t>(c.token_stride) * 2,
-                            static_cast<cuuint64_t>(c.head_stride) * 2,
-                            static_cast<cuuint64_t>(c.page_stride) * 2};
   CUtensorMap tq, tk, tv;
-  int rc = encode_4d(&tq, q, bf16, qd, qs, static_cast<unsigned>(G), static_cast<unsigned>(tt));
-  if (rc == ATTN_OK) rc = encode_4d(&tk, c.k, bf16, kd, ks, box_rows, 1);
-  if (rc == ATTN_OK) rc = encode_4d(&tv, c.v, bf16, kd, ks, box_rows, 1);
+  int rc = encode_queries(&tq, q, q_stride, c, G, total_q, tt, bf16);
+  if (rc == ATTN_OK) rc = encode_pools(&tk, &tv, c, bf16);
   if (rc != ATTN_OK) return rc;
 
   paged::Params p;

@@ -54,7 +54,7 @@ struct Cache {
   int Hkv;
   int d;
 
-  __device__ __forceinline__ long long capacity() const {
+  __host__ __device__ __forceinline__ long long capacity() const {
     return static_cast<long long>(width) << page_log2;
   }
 };
@@ -102,6 +102,16 @@ __device__ __forceinline__ int find_seq(const int* __restrict__ cu_q, int B, int
   }
   const int b = below - 1;
   return (b >= 0 && b < B) ? b : -1;
+}
+
+// 4-D tiled load of one box, completing on `bar`.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                            int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
 }
 
 }  // namespace paged
