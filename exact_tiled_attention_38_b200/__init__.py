@@ -356,318 +356,20 @@ def attn_get_device_status(stream=None) -> Tuple[int, int]:
 
 
 # ---------------------------------------------------------------- paged cache
-# A decode step makes these calls every few microseconds, so their checks are
-# kept short: one pass over the arguments, no context switch when the tensors'
-# device is the current one.
-
-def _call(fn, device, stream, *args):
-    """Run entry point `fn` with `args` and a stream on `device`."""
-    import torch
-
-    f = getattr(_lib or load_library(), fn)
-    if device.index == torch.cuda.current_device():
-        code = f(*args, _raw_stream(device) if stream is None else _stream_handle(stream))
-    else:
-        with torch.cuda.device(device):
-            code = f(*args, _raw_stream(device) if stream is None else _stream_handle(stream))
-    if code != ATTN_OK:
-        raise AttnError(code, fn)
+# These calls live in paged.py, which needs torch as it is imported; this module
+# does not, so that the library can be built without it.
+_PAGED_CALLS = ("attn_paged", "attn_rope_turns", "attn_rope", "attn_rope_bwd", "attn_rope_append",
+                "attn_pages_update", "attn_pages_compact")
 
 
-def _raw_stream(device):
-    import torch
+def __getattr__(name):
+    if name in _PAGED_CALLS:
+        from . import paged
 
-    return torch.cuda.current_stream(device).cuda_stream or None
-
-
-def _int32(t, name, device, shape):
-    import torch
-
-    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != shape or \
-            not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor {shape} on {device}")
+        globals().update({n: getattr(paged, n) for n in _PAGED_CALLS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
-def _cache(kpages, vpages, table):
-    """(_Pages, layers, layer_stride) of pools [num_pages, Hkv, page_size, d], or
-    [layers, num_pages, Hkv, page_size, d], in any strides with d innermost."""
-    import torch
-
-    dtype, device = kpages.dtype, kpages.device
-    if dtype != torch.bfloat16 and dtype != torch.float16:
-        raise ValueError("kpages and vpages must be bf16 or fp16")
-    if not kpages.is_cuda:
-        raise ValueError("kpages must be a CUDA tensor")
-    shape, strides = kpages.shape, kpages.stride()
-    if vpages.dtype != dtype or vpages.device != device or vpages.shape != shape or \
-            vpages.stride() != strides:
-        raise ValueError("vpages must have kpages' type, device, shape and strides")
-    layers, layer_stride = 1, 0
-    if len(shape) == 5:
-        layers, layer_stride = shape[0], strides[0]
-        shape, strides = shape[1:], strides[1:]
-    if len(shape) != 4 or strides[3] != 1:
-        raise ValueError("kpages must be [num_pages, Hkv, page_size, d] (or with layers in front), "
-                         "d innermost")
-    if table.dtype != torch.int32 or table.device != device or table.dim() != 2 or \
-            not table.is_contiguous():
-        raise ValueError(f"table must be a contiguous int32 tensor [B, width] on {device}")
-    P, Hkv, page, d = shape
-    # A dimension of one element has no stride that matters: give it the packed one.
-    token = strides[2] if page > 1 else d
-    head = strides[1] if Hkv > 1 else page * d
-    stride = strides[0] if P > 1 else max(Hkv * page * d, 8)
-    return (_Pages(kpages.data_ptr(), vpages.data_ptr(), table.data_ptr(), stride, head, token, P,
-                   page, table.shape[1], Hkv, d), layers, layer_stride)
-
-
-def _packed(t, name, like, heads, d):
-    """Token stride of a packed tensor [total, heads, d] whose rows may be parts of wider ones."""
-    if t.dtype != like.dtype or t.device != like.device or t.dim() != 3:
-        raise ValueError(f"{name} must be a 3-D {like.dtype} tensor [tokens, heads, d] on {like.device}")
-    if t.shape[2] != d or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must have {heads if heads is not None else 'its'} heads of {d}")
-    s = t.stride()
-    if (s[2] != 1 and d > 1) or (s[1] != d and t.shape[1] > 1):
-        raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return s[0] if t.shape[0] > 1 else t.shape[1] * d
-
-
-def attn_paged(q, kpages, vpages, table, cu_q, kv_lens, max_q: Optional[int] = None,
-               window: int = 0, scale: Optional[float] = None, o=None, lse=None, stream=None,
-               want_lse: bool = True) -> Tuple:
-    """Attention of new tokens over a paged cache (chunked prefill, decode, or a mix).
-
-    q [total, Hq, d] (bf16 or fp16; rows may be parts of wider ones), pools
-    [num_pages, Hkv, page_size, d], table [B, width], cu_q [B + 1] and kv_lens [B]
-    int32: sequence b's new tokens are rows cu_q[b]:cu_q[b + 1] of q, the last of
-    its kv_lens[b] cached positions, causal, with a sliding window if given.
-    max_q bounds the new tokens of any sequence (default: total). Returns
-    (o [total, Hq, d], lse [total, Hq]). Runs ``attn_paged`` / ``attn_paged_f16``.
-    """
-    import torch
-
-    cache, layers, _ = _cache(kpages, vpages, table)
-    if layers != 1 or kpages.dim() != 4:
-        raise ValueError("kpages must be one layer's pool [num_pages, Hkv, page_size, d]")
-    device, B = kpages.device, table.shape[0]
-    stride = _packed(q, "q", kpages, None, cache.d)
-    total, Hq, d = q.shape
-    _int32(cu_q, "cu_q", device, (B + 1,))
-    _int32(kv_lens, "kv_lens", device, (B,))
-    if o is None:
-        o = torch.empty((total, Hq, d), device=device, dtype=q.dtype)
-    elif o.dtype != q.dtype or o.device != device or o.shape != q.shape or not o.is_contiguous():
-        raise ValueError("o must be a contiguous tensor of q's shape, type and device")
-    if lse is None:
-        if want_lse:
-            lse = torch.empty((total, Hq), device=device, dtype=torch.float32)
-    elif lse.dtype != torch.float32 or lse.device != device or \
-            tuple(lse.shape) != (total, Hq) or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 tensor [total, Hq] on q's device")
-    _call("attn_paged_f16" if q.dtype == torch.float16 else "attn_paged", device, stream,
-          q.data_ptr(), stride, cache, cu_q.data_ptr(), kv_lens.data_ptr(), o.data_ptr(),
-          lse.data_ptr() if lse is not None else None, B, Hq, total,
-          total if max_q is None else int(max_q),
-          1.0 / math.sqrt(d) if scale is None else float(scale), int(window))
-    return o, lse
-
-
-def attn_rope_turns(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
-                    low: float = 1.0, high: Optional[float] = None, original: float = 4096.0):
-    """Turns per position of each rotary pair (float64, on the CPU) and the amplitude.
-
-    scaling: "none", "linear", "base", "parts" (high defaults to 32) or "bands"
-    (high defaults to 4); see ``attn_rope_turns`` in include/attn.h.
-    """
-    import torch
-
-    names = ("none", "linear", "base", "parts", "bands")
-    if scaling not in names:
-        raise ValueError(f"scaling must be one of {names}")
-    if high is None:
-        high = 32.0 if scaling == "parts" else 4.0
-    buf = (_D * max(rot // 2, 1))()
-    amp = _F(0.0)
-    code = load_library().attn_rope_turns(buf, ctypes.byref(amp), int(rot), float(base),
-                                          names.index(scaling), float(factor), float(low),
-                                          float(high), float(original))
-    _check(code, "attn_rope_turns")
-    return torch.tensor(list(buf), dtype=torch.float64), amp.value
-
-
-def _turns_of(turns, device, d):
-    import torch
-
-    if turns.dtype != torch.float64 or turns.device != device or turns.dim() != 1 or \
-            not turns.is_contiguous():
-        raise ValueError(f"turns must be a contiguous float64 tensor [rot / 2] on {device}")
-    rot = 2 * turns.shape[0]
-    if rot > d:
-        raise ValueError("turns must have at most d / 2 entries")
-    return rot
-
-
-def _rope(q, k, pos, turns, amp, interleaved, q_out, k_out, stream, backward):
-    import torch
-
-    dtype, device = q.dtype, q.device
-    if dtype != torch.bfloat16 and dtype != torch.float16:
-        raise ValueError("q must be bf16 or fp16")
-    if not q.is_cuda:
-        raise ValueError("q must be a CUDA tensor")
-    if q.dim() != 4:
-        raise ValueError("q must be a 4-D tensor [B, H, N, d]")
-    B, Hq, N, d = q.shape
-    Hkv = 0
-    if k is not None:
-        if k.dim() != 4 or k.dtype != dtype or k.device != device or \
-                (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d):
-            raise ValueError("k must be [B, Hkv, N, d] of q's B, N, d, type and device")
-        Hkv = k.shape[1]
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    if q_out is None:
-        q_out = torch.empty((B, Hq, N, d), device=device, dtype=dtype)
-    if k is not None and k_out is None:
-        k_out = torch.empty((B, Hkv, N, d), device=device, dtype=dtype)
-    strides = (_L * 12)()
-    at = 0
-    for t, like in ((q, q), (q_out, q), (k, k), (k_out, k)):
-        if t is not None:
-            if t.shape != like.shape or t.dtype != dtype or t.device != device:
-                raise ValueError("an output must have its input's shape, type and device")
-            s, n = t.stride(), t.shape
-            if s[3] != 1 and d > 1:
-                raise ValueError("the last dimension of q, k and the outputs must be contiguous")
-            # A dimension of one element has no stride that matters.
-            strides[at] = s[0] if n[0] > 1 else 0
-            strides[at + 1] = s[1] if n[1] > 1 else 0
-            strides[at + 2] = s[2] if n[2] > 1 else 0
-        at += 3
-    if pos.dtype != torch.int32 or pos.device != device or not pos.is_contiguous() or \
-            tuple(pos.shape) not in ((N,), (B, N)):
-        raise ValueError(f"pos must be a contiguous int32 tensor [N] or [B, N] on {device}")
-    rot = _turns_of(turns, device, d)
-    _call("attn_rope_f16" if dtype == torch.float16 else "attn_rope", device, stream,
-          q.data_ptr(), q_out.data_ptr(), k.data_ptr() if k is not None else None,
-          k_out.data_ptr() if k is not None else None, strides, pos.data_ptr(),
-          N if pos.dim() == 2 else 0, turns.data_ptr(), B, Hq, Hkv, N, d, rot, float(amp),
-          1 if interleaved else 0, backward)
-    return q_out, k_out
-
-
-def attn_rope(q, k, pos, turns, amp: float = 1.0, interleaved: bool = False, q_out=None,
-              k_out=None, stream=None) -> Tuple:
-    """Rotary positions of q [B, Hq, N, d] and k [B, Hkv, N, d] (or None), bf16 or fp16.
-
-    Any strides with d innermost; an output may be its input. pos int32 [N] or
-    [B, N]; turns and amp from ``attn_rope_turns`` (turns on q's device): the
-    first 2 * len(turns) values of each head are rotated. Returns (q_out, k_out).
-    """
-    return _rope(q, k, pos, turns, amp, interleaved, q_out, k_out, stream, 0)
-
-
-def attn_rope_bwd(dq, dk, pos, turns, amp: float = 1.0, interleaved: bool = False, dq_in=None,
-                  dk_in=None, stream=None) -> Tuple:
-    """Gradients of ``attn_rope``'s inputs from those of its outputs (same arguments)."""
-    return _rope(dq, dk, pos, turns, amp, interleaved, dq_in, dk_in, stream, 1)
-
-
-def attn_rope_append(q, k, v, kpages, vpages, table, cu_q, kv_lens, turns, amp: float = 1.0,
-                     interleaved: bool = False, pos=None, q_out=None, stream=None):
-    """Rotate new tokens' q and k, and put k and v into the paged cache, in one pass.
-
-    q [total, Hq, d], k and v [total, Hkv, d] (rows may be parts of wider ones, as
-    one projection gives them); cache arguments as in ``attn_paged``. Positions
-    are the tokens' places in the cache unless pos (int32 [total]) is given.
-    Returns q_out; the pools are updated in place.
-    """
-    import torch
-
-    cache, layers, _ = _cache(kpages, vpages, table)
-    if layers != 1 or kpages.dim() != 4:
-        raise ValueError("kpages must be one layer's pool [num_pages, Hkv, page_size, d]")
-    device, B, d = kpages.device, table.shape[0], cache.d
-    total, Hq = q.shape[0], q.shape[1] if q.dim() == 3 else 0
-    qs = _packed(q, "q", kpages, None, d)
-    ks = _packed(k, "k", kpages, cache.Hkv, d)
-    vs = _packed(v, "v", kpages, cache.Hkv, d)
-    if k.shape[0] != total or v.shape[0] != total:
-        raise ValueError("q, k and v must have the same tokens")
-    _int32(cu_q, "cu_q", device, (B + 1,))
-    _int32(kv_lens, "kv_lens", device, (B,))
-    if pos is not None:
-        _int32(pos, "pos", device, (total,))
-    if q_out is None:
-        q_out = torch.empty((total, Hq, d), device=device, dtype=q.dtype)
-    elif q_out.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
-    os_ = _packed(q_out, "q_out", kpages, Hq, d)
-    rot = _turns_of(turns, device, d)
-    _call("attn_rope_append_f16" if q.dtype == torch.float16 else "attn_rope_append", device,
-          stream, q.data_ptr(), qs, q_out.data_ptr(), os_, k.data_ptr(), ks, v.data_ptr(), vs,
-          cache, cu_q.data_ptr(), kv_lens.data_ptr(), pos.data_ptr() if pos is not None else None,
-          turns.data_ptr(), B, Hq, total, rot, float(amp), 1 if interleaved else 0)
-    return q_out
-
-
-def attn_pages_update(kpages, vpages, table, lens, refs, source, add, table_out=None,
-                      lens_out=None, refs_out=None, info=None, stream=None) -> Tuple:
-    """One step of the cache's bookkeeping: row b of the next state goes on from
-    row source[b] (-1: from nothing) and grows by add[b] tokens; shared last pages
-    are copied in every layer. Pools [layers, num_pages, Hkv, page_size, d] or one
-    layer's; table [B, width], lens, source, add [B], refs [num_pages], int32.
-    Returns (table, lens, refs, info) of the next state; info [2] is zero, or the
-    pages that were missing and the rows that outgrew the table (nothing changed
-    then). See ``attn_pages_update`` in include/attn.h.
-    """
-    import torch
-
-    cache, layers, layer_stride = _cache(kpages, vpages, table)
-    device, B = kpages.device, table.shape[0]
-    for t, n, size in ((lens, "lens", B), (refs, "refs", cache.num_pages),
-                       (source, "source", B), (add, "add", B)):
-        _int32(t, n, device, (size,))
-    if table_out is None:
-        table_out = torch.empty_like(table)
-    if lens_out is None:
-        lens_out = torch.empty_like(lens)
-    if refs_out is None:
-        refs_out = torch.empty_like(refs)
-    if info is None:
-        info = torch.empty(2, dtype=torch.int32, device=device)
-    for t, n, shape in ((table_out, "table_out", tuple(table.shape)), (lens_out, "lens_out", (B,)),
-                        (refs_out, "refs_out", (cache.num_pages,)), (info, "info", (2,))):
-        _int32(t, n, device, shape)
-    _call("attn_pages_update", device, stream, cache, layers, layer_stride, lens.data_ptr(),
-          refs.data_ptr(), source.data_ptr(), add.data_ptr(), table_out.data_ptr(),
-          lens_out.data_ptr(), refs_out.data_ptr(), info.data_ptr(), B)
-    return table_out, lens_out, refs_out, info
-
-
-def attn_pages_compact(kpages, vpages, table, lens, refs, table_out=None, refs_out=None, info=None,
-                       stream=None) -> Tuple:
-    """Move the live pages to the lowest indices, in every layer, with the fewest copies.
-
-    Arguments as in ``attn_pages_update``. Returns (table, refs, info) of the next
-    state; info [2]: live pages, moved pages.
-    """
-    import torch
-
-    cache, layers, layer_stride = _cache(kpages, vpages, table)
-    device, B = kpages.device, table.shape[0]
-    _int32(lens, "lens", device, (B,))
-    _int32(refs, "refs", device, (cache.num_pages,))
-    if table_out is None:
-        table_out = torch.empty_like(table)
-    if refs_out is None:
-        refs_out = torch.empty_like(refs)
-    if info is None:
-        info = torch.empty(2, dtype=torch.int32, device=device)
-    for t, n, shape in ((table_out, "table_out", tuple(table.shape)),
-                        (refs_out, "refs_out", (cache.num_pages,)), (info, "info", (2,))):
-        _int32(t, n, device, shape)
-    _call("attn_pages_compact", device, stream, cache, layers, layer_stride, lens.data_ptr(),
-          refs.data_ptr(), table_out.data_ptr(), refs_out.data_ptr(), info.data_ptr(), B)
-    return table_out, refs_out, info
+def __dir__():
+    return sorted({*globals(), *_PAGED_CALLS})

@@ -134,8 +134,11 @@ int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (attr_err != cudaSuccess) return cuda_fail(attr_err);
-  paged::attn_paged_plan_kernel<<<1, paged::kPlanThreads, 0, st>>>(p);
-  int rc = launch_status();
+  int rc = ATTN_OK;
+  if (!p.inline_plan) {
+    paged::attn_paged_plan_kernel<<<1, paged::kPlanThreads, 0, st>>>(p);
+    rc = launch_status();
+  }
   if (rc == ATTN_OK)
     rc = launch_dependent(kern, dim3(static_cast<unsigned>(p.nc)), paged::kThreads, smem, st, tq,
                           tk, tv, p);
@@ -252,6 +255,11 @@ int paged_run(const void* q, long long q_stride, const attn_pages* pages, const 
 
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   const int tt = paged::BM / G;
+  // (a CTA's steps are counted in 32 bits: with the longest cache that the
+  // table allows for every token, this is years of work)
+  if ((static_cast<double>(total_q) / (paged::NQT * tt) + B) * c.Hkv *
+          (static_cast<double>(c.capacity()) / paged::BN + 1) / info.sm_count > 2e9)
+    return ATTN_ERR_UNSUPPORTED;
   CUtensorMap tq, tk, tv;
   int rc = encode_queries(&tq, q, q_stride, c, G, total_q, tt, bf16);
   if (rc == ATTN_OK) rc = encode_pools(&tk, &tv, c, bf16);
@@ -276,25 +284,31 @@ int paged_run(const void* q, long long q_stride, const attn_pages* pages, const 
   p.width = c.width;
   p.window = window;
   p.nc = info.sm_count;
+  p.inline_plan = B <= paged::kInlineB ? 1 : 0;
+  p.max_pairs = (max_q + paged::NQT * tt - 1) / (paged::NQT * tt);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_ns = kDefaultWaitNs;
-  // Workspace: the plan, then two slots of partial rows per CTA.
+  p.l2_bytes = info.l2_bytes;
+  // Workspace: the plan, then three slots of partial rows per CTA.
   size_t end = 0;
   const auto part = [&end](size_t bytes) {
     const size_t at = end;
     end = align_up(end + bytes, 256);
     return at;
   };
-  const size_t slots = static_cast<size_t>(2) * p.nc * paged::kSlotRows;
-  const size_t cost = part((static_cast<size_t>(B) + 1) * 8), starts = part(p.nc * sizeof(int4)),
-               busy = part(4), part_lse = part(slots * 4), part_o = part(slots * c.d * 4);
+  const size_t slots = static_cast<size_t>(3) * p.nc * paged::kSlotRows;
+  const size_t head = part(sizeof(paged::Head)), starts = part(p.nc * sizeof(paged::Start)),
+               rest_at = part(p.inline_plan ? 0 : (static_cast<size_t>(B) + 1) * 8),
+               chunk_at = part(p.inline_plan ? 0 : (static_cast<size_t>(B) + 1) * 4),
+               part_lse = part(slots * 4), part_o = part(slots * c.d * 4);
   Workspace ws;
   rc = ws.take(end, st);
   if (rc != ATTN_OK) return rc;
   char* base = static_cast<char*>(ws.p);
-  p.plan.cost = reinterpret_cast<long long*>(base + cost);
-  p.plan.starts = reinterpret_cast<int4*>(base + starts);
-  p.plan.busy = reinterpret_cast<int*>(base + busy);
+  p.plan.head = reinterpret_cast<paged::Head*>(base + head);
+  p.plan.starts = reinterpret_cast<paged::Start*>(base + starts);
+  p.plan.rest_at = reinterpret_cast<long long*>(base + rest_at);
+  p.plan.chunk_at = reinterpret_cast<int*>(base + chunk_at);
   p.part_lse = reinterpret_cast<float*>(base + part_lse);
   p.part_o = reinterpret_cast<float*>(base + part_o);
   rc = c.d <= 64 ? launch_paged<64, T>(tq, tk, tv, p, st) : launch_paged<128, T>(tq, tk, tv, p, st);

@@ -11,17 +11,28 @@
 // token, so that the whole group shares each key tile read: a tile of 128 rows
 // holds tt = 128 / G tokens. A work item is a pair of such tiles of one
 // sequence and KV head; its steps are the tiles of 128 keys that any of its
-// rows sees. The steps of all items, in order (sequence, KV head, tile pair,
-// key tile), are cut into equal contiguous ranges, one per CTA (one CTA per
-// SM): a chunk over a long cache then fills the GPU however few rows it has,
-// and a mixed batch is balanced. A piece that is not a whole item leaves a
-// normalised fp32 partial with its log-sum-exp, and the gather kernel folds
-// the partials of an item together in the order of its keys.
+// rows sees. Every CTA (one per SM) gets the same number w of steps, so that a
+// chunk over a long cache fills the GPU however few rows it has and a mixed
+// batch is balanced. The steps are dealt out in one of two ways:
+//   - in order (sequence, KV head, tile pair, key tile), in contiguous ranges;
+//   - when the batch's keys and values exceed what L2 can hold, an item of
+//     n >= w steps first gives floor(n / w) chunks of w, a CTA each, and only
+//     the rests go in contiguous ranges to the CTAs left. The pairs of a head
+//     then run over the same keys at the same time, and all but the first find
+//     them in L2. (1024 tokens over 64K, 32/8 heads: in contiguous ranges each
+//     CTA was at another key, 3.9 GB came from DRAM where q, k and v have 0.28.)
+// For the same reason a CTA that has done s steps begins a whole item of n at
+// its key tile s mod n and wraps around: CTAs that work on one head stay
+// together although they began their items at different times.
+// A piece that is not a whole item leaves a normalised fp32 partial with its
+// log-sum-exp, and the gather kernel folds the partials of an item together in
+// the order of its keys.
 //
-// Three kernels per call:
-//   attn_paged_plan_kernel    one CTA: steps of each sequence, their prefix
-//                             sums, each CTA's first (sequence, head, pair, step)
-//   attn_paged_kernel         the stream (below)
+// Two or three kernels per call:
+//   attn_paged_plan_kernel    (batches above kInlineB sequences) one CTA: the
+//                             steps, w, and where each CTA begins
+//   attn_paged_kernel         the stream (below); for smaller batches each CTA
+//                             works out the plan, and its own start, itself
 //   attn_paged_gather_kernel  the cut items
 //
 // The stream has the warp roles of the prefill kernel: warps 0-3 and 4-7 are
@@ -34,6 +45,10 @@
 // loaded at an out-of-range coordinate, which fills zeros and reads nothing.
 //   Two tiles of rows (pair): both groups work on every key tile, S_t = Q_t K^T
 // and O_t += P_t V, as in the prefill kernel.
+//   With D = 64 tensor memory has room for P beside S: S_t is released as soon
+// as it has been read, so the next scores run during the exponentials (s_free),
+// and P_t waits for the previous product instead (pv_done). With D = 128 P
+// overwrites S.
 //   One tile of rows (a single token, or a short chunk): the groups share Q_0
 // and take the key tiles in turns, each with its own running maximum, sum and
 // O; group 0 folds O_1 into O_0 at the end of the piece. One group's
@@ -58,6 +73,7 @@ constexpr int kMmaWarp = 8;
 constexpr int kTmaWarp = 9;
 constexpr int kPlanThreads = 1024;
 constexpr int kSlotRows = NQT * BM;
+constexpr int kInlineB = 2048;  // batches up to this many sequences plan in the stream kernel
 
 // Wait sites reported in the status word.
 enum : unsigned {
@@ -71,6 +87,8 @@ enum : unsigned {
   kSiteQEmpty = 0x88,
   kSiteXUp = 0x89,
   kSiteXDown = 0x8a,
+  kSiteSFree = 0x8b,
+  kSitePvDone = 0x8c,
 };
 
 template <int D>
@@ -85,23 +103,49 @@ struct Cfg {
   static constexpr int kStgOff = kKVOff + kStages * kTileBytes;
   static constexpr int kBarOff = kStgOff + 8 * kStgWarpBytes;
   // kv_full[S], kv_empty[S], q_full[2], q_empty[2], s_ready[2], p_ready[2],
-  // o_done[2], x_up, x_down, drain
-  static constexpr int kNumBars = 2 * kStages + 5 * NQT + 3;
+  // o_done[2], s_free[2], pv_done[2], x_up, x_down, drain
+  static constexpr int kNumBars = 2 * kStages + 7 * NQT + 3;
   static constexpr int kCtlOff = kBarOff + kNumBars * 8;
-  static constexpr int kXOff = kCtlOff + 64;  // (m, l) of group 1's rows
-  static constexpr int kSmemBytes = kXOff + BM * 8 + 1024;  // + runtime 1024-byte alignment
+  // (m, l) of group 1's rows, where its output would be staged (it stages none then).
+  static constexpr int kXOff = kStgOff + 4 * kStgWarpBytes;
+  static constexpr int kWalkOff = kCtlOff + 64;  // each warp's way through the range
+  static constexpr int kSmemBytes = kWalkOff + 10 * 80 + 1024;  // + runtime 1024-byte alignment
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kPCol = 64;  // P_t overwrites S_t from this column on
-  __host__ __device__ static constexpr uint32_t s_col(int t) { return BN * t; }
-  __host__ __device__ static constexpr uint32_t o_col(int t) { return 2 * BN + D * t; }
+  static constexpr bool kOwnP = D == 64;  // P in columns of its own, else over S from column 64 on
+  __host__ __device__ static constexpr uint32_t s_col(int t) { return kOwnP ? 256u * t : BN * t; }
+  __host__ __device__ static constexpr uint32_t p_col(int t) {
+    return kOwnP ? 256u * t + BN : BN * t + 64u;
+  }
+  __host__ __device__ static constexpr uint32_t o_col(int t) {
+    return kOwnP ? 256u * t + BN + 64u : 2 * BN + D * t;
+  }
+  // The inline plan's prefix sums lie where the output is staged later.
+  static_assert((kInlineB + 1) * 12 <= 8 * kStgWarpBytes, "plan scratch");
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
+// Where a CTA begins.
+struct alignas(16) Start {
+  int b, g, pair;
+  int i;           // step of the item
+  int chunk;       // the first chunk CTA of the item, or of the next that has one
+  int pad;
+  long long rest;  // rests before the item's
+};
+
 // The plan, in device memory.
+struct Head {
+  long long steps;  // of all items
+  long long w;      // steps of a CTA
+  long long rest;   // steps that are not in chunks
+  int chunks;       // CTAs that take a chunk: 0 .. chunks - 1; the rests follow
+  int ctas;         // CTAs with work
+};
 struct Plan {
-  long long* cost;  // [B + 1]: steps before sequence b (all its KV heads)
-  int4* starts;     // [nc]: (b, g, pair, step) where CTA c begins
-  int* busy;        // [1]: CTAs that have a range (min(nc, steps))
+  Head* head;
+  Start* starts;       // [nc]
+  long long* rest_at;  // [B + 1] (plan kernel): rests before each sequence
+  int* chunk_at;       // [B + 1] (plan kernel): chunks before each sequence
 };
 
 struct Params {
@@ -110,14 +154,17 @@ struct Params {
   const int* table;
   void* o;
   float* lse;
-  float* part_o;    // [2 nc][256][d]
-  float* part_lse;  // [2 nc][256], log2 units
+  float* part_o;    // [3 nc][256][d]
+  float* part_lse;  // [3 nc][256], log2 units
   Plan plan;
   int B, Hq, Hkv, G, tt;
   int total_q, max_q, d;
   int num_pages, page_log2, width;
   int window;
   int nc;
+  int inline_plan;  // no plan kernel
+  int max_pairs;    // tile pairs that a sequence of max_q tokens has
+  long long l2_bytes;
   float scale_log2;
   uint64_t wait_ns;
 
@@ -144,159 +191,305 @@ __device__ __forceinline__ int pairs_of(const Params& p, int T) {
   return (T + NQT * p.tt - 1) / (NQT * p.tt);
 }
 
-// Steps of one KV head of a sequence, by the whole warp.
-__device__ __forceinline__ long long seq_steps(const Params& p, const Seq& s, int lane) {
-  const int n = pairs_of(p, s.T);
-  long long sum = 0;
-  for (int i = lane; i < n; i += 32) sum += span_of(p, s, i).n;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum;
+// n / d for 0 <= n, 0 < d, in 32 bits when both fit (the usual case).
+__device__ __forceinline__ long long div_pos(long long n, long long d) {
+  if (((n | d) >> 31) == 0)
+    return static_cast<long long>(static_cast<unsigned>(n) / static_cast<unsigned>(d));
+  return n / d;
 }
 
-__device__ __forceinline__ long long range_lo(int c, long long steps, int busy) {
-  return c * steps / busy;
+// Chunks of w steps in an item of n (0: the item goes to the rests whole).
+__device__ __forceinline__ int chunks_of(int n, long long w, bool chunked) {
+  return chunked && n >= w ? static_cast<int>(static_cast<unsigned>(n) / static_cast<unsigned>(w)) : 0;
 }
 
 // A range of fewer steps than this is not worth a CTA of its own.
 constexpr int kMinSteps = 2;
 
-__global__ void __launch_bounds__(kPlanThreads) attn_paged_plan_kernel(const Params p) {
-  __shared__ long long red[kPlanThreads / 32];
-  grid_launch_dependents();
+// Sums over a block of (a, b), which every thread gets; `red` holds 2 THREADS / 32 words.
+template <int THREADS>
+__device__ __forceinline__ void block_sum(long long& a, long long& b, long long* red) {
+  constexpr int W = THREADS / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  __syncthreads();  // red's last use
+  if (lane == 0) {
+    red[2 * warp] = a;
+    red[2 * warp + 1] = b;
+  }
+  __syncthreads();
+  a = b = 0;
+#pragma unroll 4
+  for (int w = 0; w < W; ++w) {
+    a += red[2 * w];
+    b += red[2 * w + 1];
+  }
+}
+
+// The plan, by a whole block of THREADS: its head, and the chunks and rests
+// before each sequence (rest_at, chunk_at [B + 1]).
+template <int THREADS>
+__device__ __forceinline__ Head make_plan(const Params& p, long long* rest_at, int* chunk_at,
+                                          long long* red, bool check) {
+  constexpr int W = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int b = warp; b < p.B; b += kPlanThreads / 32) {
+  // A thread per sequence; a warp per sequence where they have many tile pairs.
+  const bool wide = p.max_pairs > 32;
+  const int b_first = wide ? warp : tid, b_step = wide ? W : THREADS;
+  const int i_first = wide ? lane : 0, i_step = wide ? 32 : 1;
+  long long steps = 0, keys = 0;
+  for (int b = b_first; b < p.B; b += b_step) {
     const Seq s = load_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
-    const long long c = seq_steps(p, s, lane) * p.Hkv;
-    if (lane == 0) {
-      p.plan.cost[b] = c;
-      check_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
+    const int n = pairs_of(p, s.T);
+    for (int i = i_first; i < n; i += i_step) steps += span_of(p, s, i).n;
+    if (i_first == 0) {
+      keys += s.T > 0 ? s.L : 0;
+      if (check) check_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
+    }
+  }
+  block_sum<THREADS>(steps, keys, red);
+  Head h;
+  h.steps = steps * p.Hkv;
+  const long long want = div_pos(h.steps + kMinSteps - 1, kMinSteps);
+  const int busy = static_cast<int>(want < p.nc ? want : p.nc);
+  h.w = busy > 0 ? div_pos(h.steps + busy - 1, busy) : 1;
+  // Keys and values beyond half of L2 will not stay in it between two CTAs
+  // that come by at different times.
+  const bool chunked = keys * p.Hkv * p.d * 4 > p.l2_bytes / 2;
+  for (int b = b_first; b < p.B; b += b_step) {
+    const Seq s = load_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
+    const int n = pairs_of(p, s.T);
+    long long rest = 0;
+    int chunks = 0;
+    for (int i = i_first; i < n; i += i_step) {
+      const int k = span_of(p, s, i).n, f = chunks_of(k, h.w, chunked);
+      chunks += f;
+      rest += k - f * h.w;
+    }
+    if (wide) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        rest += __shfl_xor_sync(0xffffffffu, rest, o);
+        chunks += __shfl_xor_sync(0xffffffffu, chunks, o);
+      }
+    }
+    if (i_first == 0) {
+      rest_at[b] = rest * p.Hkv;
+      chunk_at[b] = chunks * p.Hkv;
     }
   }
   __syncthreads();
   // Exclusive prefix over the sequences, in place.
-  const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
+  const int per = (p.B + THREADS - 1) / THREADS;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += p.plan.cost[b];
-  long long x = mine;
+  long long rest = 0, chunks = 0;
+  for (int b = b0; b < b1; ++b) {
+    rest += rest_at[b];
+    chunks += chunk_at[b];
+  }
+  long long x = rest, y = chunks;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const long long x2 = __shfl_up_sync(0xffffffffu, x, o);
+    const long long y2 = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) {
+      x += x2;
+      y += y2;
+    }
   }
-  if (lane == 31) red[warp] = x;
+  if (lane == 31) {
+    red[2 * warp] = x;
+    red[2 * warp + 1] = y;
+  }
   __syncthreads();
-  if (warp == 0) {
-    long long w = red[lane];
+  long long xb = 0, yb = 0, xa = 0, ya = 0;
+#pragma unroll 4
+  for (int w = 0; w < W; ++w) {
+    const long long u = red[2 * w], v = red[2 * w + 1];
+    if (w < warp) {
+      xb += u;
+      yb += v;
+    }
+    xa += u;
+    ya += v;
+  }
+  x += xb - rest;
+  y += yb - chunks;
+  for (int b = b0; b < b1; ++b) {
+    const long long r = rest_at[b];
+    const int k = chunk_at[b];
+    rest_at[b] = x;
+    chunk_at[b] = static_cast<int>(y);
+    x += r;
+    y += k;
+  }
+  if (tid == 0) {
+    rest_at[p.B] = xa;
+    chunk_at[p.B] = static_cast<int>(ya);
+  }
+  h.rest = xa;
+  h.chunks = static_cast<int>(ya);
+  h.ctas = h.chunks + static_cast<int>(div_pos(xa + h.w - 1, h.w));
+  __syncthreads();
+  return h;
+}
+
+// Where CTA c (of those with work) begins, by a whole warp.
+__device__ __forceinline__ Start plan_find(const Params& p, const Head& h, const long long* rest_at,
+                                           const int* chunk_at, int c, int lane) {
+  const bool chunked = h.chunks > 0, mine = c < h.chunks;
+  const long long at = mine ? c : (c - h.chunks) * h.w;  // among the chunks, or the rests
+  int lo = 0, hi = p.B - 1;  // the last sequence that begins at or before `at`
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((mine ? chunk_at[mid] : rest_at[mid]) <= at)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const Seq s = load_seq(p.cu_q, p.lens, lo, p.total_q, p.max_q, p.capacity());
+  const long long rest_head = div_pos(rest_at[lo + 1] - rest_at[lo], p.Hkv);
+  const int chunk_head = (chunk_at[lo + 1] - chunk_at[lo]) / p.Hkv;
+  long long r = mine ? c - chunk_at[lo] : at - rest_at[lo];
+  const long long per_head = mine ? chunk_head : rest_head;
+  Start st;
+  st.b = lo;
+  st.g = static_cast<int>(div_pos(r, per_head));
+  st.pad = 0;
+  r -= st.g * per_head;
+  st.rest = rest_at[lo] + st.g * rest_head;
+  st.chunk = chunk_at[lo] + st.g * chunk_head;
+  st.pair = 0;
+  st.i = 0;
+  const int n = pairs_of(p, s.T);
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int k = i0 + lane < n ? span_of(p, s, i0 + lane).n : 0;
+    const int f = chunks_of(k, h.w, chunked);
+    const int rr = static_cast<int>(k - f * h.w);  // (32 spans stay below 2^31)
+    int x = rr, y = f;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    red[lane] = w;
-  }
-  __syncthreads();
-  const long long steps = red[kPlanThreads / 32 - 1];
-  long long run = x - mine + (warp > 0 ? red[warp - 1] : 0);
-  for (int b = b0; b < b1; ++b) {
-    const long long c = p.plan.cost[b];
-    p.plan.cost[b] = run;
-    run += c;
-  }
-  const long long want = (steps + kMinSteps - 1) / kMinSteps;
-  const int busy = static_cast<int>(want < p.nc ? want : p.nc);
-  if (tid == 0) {
-    p.plan.cost[p.B] = steps;
-    *p.plan.busy = busy;
-  }
-  __syncthreads();
-  // Where each CTA begins: the sequence by bisection, the tile pair by a scan.
-  for (int c = warp; c < busy; c += kPlanThreads / 32) {
-    const long long at = range_lo(c, steps, busy);
-    int lo = 0, hi = p.B - 1;  // largest b with cost[b] <= at
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.plan.cost[mid] <= at)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    const long long per_head = (p.plan.cost[lo + 1] - p.plan.cost[lo]) / p.Hkv;
-    long long r = at - p.plan.cost[lo];
-    const int g = static_cast<int>(r / per_head);
-    r -= g * per_head;
-    const Seq s = load_seq(p.cu_q, p.lens, lo, p.total_q, p.max_q, p.capacity());
-    const int n = pairs_of(p, s.T);
-    int pair = 0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int k = i0 + lane < n ? span_of(p, s, i0 + lane).n : 0;
-      int y = k;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
+      const int x2 = __shfl_up_sync(0xffffffffu, x, o);
+      const int y2 = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) {
+        x += x2;
+        y += y2;
       }
-      const unsigned over = __ballot_sync(0xffffffffu, r < y);  // (32 spans stay below 2^31)
-      if (over != 0) {
-        const int l = __ffs(over) - 1;
-        r -= __shfl_sync(0xffffffffu, y - k, l);
-        pair = i0 + l;
-        break;
-      }
-      r -= __shfl_sync(0xffffffffu, y, 31);
     }
-    if (lane == 0) p.plan.starts[c] = make_int4(lo, g, pair, static_cast<int>(r));
+    const unsigned over = __ballot_sync(0xffffffffu, r < (mine ? y : x));
+    if (over != 0) {
+      const int l = __ffs(over) - 1;
+      st.pair = i0 + l;
+      st.rest += __shfl_sync(0xffffffffu, x - rr, l);
+      st.chunk += __shfl_sync(0xffffffffu, y - f, l);
+      const int before = __shfl_sync(0xffffffffu, mine ? y - f : x - rr, l);
+      const int fl = __shfl_sync(0xffffffffu, f, l);
+      st.i = static_cast<int>(mine ? (r - before) * h.w : fl * h.w + (r - before));
+      break;
+    }
+    r -= __shfl_sync(0xffffffffu, mine ? y : x, 31);
+    st.rest += __shfl_sync(0xffffffffu, x, 31);
+    st.chunk += __shfl_sync(0xffffffffu, y, 31);
+  }
+  return st;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) attn_paged_plan_kernel(const Params p) {
+  __shared__ long long red[2 * kPlanThreads / 32];
+  grid_launch_dependents();
+  const Head h = make_plan<kPlanThreads>(p, p.plan.rest_at, p.plan.chunk_at, red, true);
+  if (threadIdx.x == 0) *p.plan.head = h;
+  for (int c = threadIdx.x >> 5; c < h.ctas; c += kPlanThreads / 32) {
+    const Start st = plan_find(p, h, p.plan.rest_at, p.plan.chunk_at, c, threadIdx.x & 31);
+    if ((threadIdx.x & 31) == 0) p.plan.starts[c] = st;
   }
 }
 
-// A CTA's way through its range, piece by piece. Every role keeps its own.
+// A CTA's way through its range, piece by piece. Every warp keeps its own, in
+// shared memory (in registers it would push the softmax's scores out): lane 0
+// moves it on, the others read it.
 struct Walk {
   int b, g, pair;
   int i0, i1, n;   // steps [i0, i1) of the item's n
+  int first;       // the item's first step outside its chunks
   int lo;          // its first key tile
-  long long left;  // steps of the range behind this piece
+  int rot;         // the piece begins at its step rot and wraps around
+  int chunk;       // the item's first chunk CTA (if it has chunks)
+  int more;        // this is a piece (0: the range has ended)
+  int w;           // steps of a chunk (0: no item has any)
+  int left;        // steps of the range behind this piece
+  int done;        // and up to its end
   Seq s;
 
-  __device__ __forceinline__ void item(const Params& p, int from) {
+  __device__ __forceinline__ void item(const Params& p) {
     const Span sp = span_of(p, s, pair);
     lo = sp.lo;
     n = sp.n;
+    first = w > 0 && n >= w ? n - static_cast<int>(static_cast<unsigned>(n) % static_cast<unsigned>(w)) : 0;
+  }
+  __device__ __forceinline__ void piece(int from) {
     i0 = from;
-    i1 = static_cast<int>(min(static_cast<long long>(n), i0 + left));
+    i1 = min(n, i0 + left);
     left -= i1 - i0;
+    rot = i0 == first && i1 == n ? done % (n - first) : 0;
+    done += i1 - i0;
   }
-  __device__ __forceinline__ void start(const Params& p, int c, long long count) {
-    const int4 st = p.plan.starts[c];
-    b = st.x, g = st.y, pair = st.z;
-    left = count;
+  __device__ __forceinline__ void start(const Params& p, const Head& h, const Start& st, int c) {
+    b = st.b, g = st.g, pair = st.pair, chunk = st.chunk;
+    w = h.chunks > 0 ? static_cast<int>(h.w) : 0;
+    const long long rest = h.rest - (c - h.chunks) * h.w;
+    left = static_cast<int>(c < h.chunks || rest > h.w ? h.w : rest);
+    done = 0;
+    more = 1;
     s = load_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
-    item(p, st.w);
+    item(p);
+    piece(st.i);
   }
-  // To the next piece; false at the end of the range.
-  __device__ __forceinline__ bool next(const Params& p) {
-    if (left <= 0) return false;
-    if (++pair >= pairs_of(p, s.T)) {
-      pair = 0;
-      if (++g >= p.Hkv) {
-        g = 0;
-        do {
-          if (++b >= p.B) return false;  // (the plan's range ends before this)
-          s = load_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
-        } while (s.T == 0);
+  __device__ __forceinline__ void next(const Params& p) {
+    more = 0;
+    if (left <= 0) return;
+    do {  // (an item may be all chunks)
+      if (w > 0) chunk += first / w;
+      if (++pair >= pairs_of(p, s.T)) {
+        pair = 0;
+        if (++g >= p.Hkv) {
+          g = 0;
+          do {
+            if (++b >= p.B) return;  // (the plan's range ends before this)
+            s = load_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
+          } while (s.T == 0);
+        }
       }
-    }
-    item(p, 0);
-    return true;
+      item(p);
+    } while (first == n);
+    piece(first);
+    more = 1;
   }
-  __device__ __forceinline__ int token0() const { return pair; }
   __device__ __forceinline__ int steps() const { return i1 - i0; }
   __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == n; }
+  // The slot of a piece that is not the whole item, in CTA c of nc: a chunk or
+  // what goes on from the CTA before, what goes on in the next, all of a rest.
+  __device__ __forceinline__ int slot(int c, int nc, int chunks) const {
+    return c < chunks || i0 != first ? c : i1 < n ? nc + c : 2 * nc + chunk;
+  }
   // Both tiles have rows?
   __device__ __forceinline__ bool two(const Params& p) const {
     return pair * NQT * p.tt + p.tt < s.T;
   }
 };
+static_assert(sizeof(Walk) <= 80, "shared memory of a warp's walk");
+
+// The warp's walk to its next piece; false at the end of the range.
+__device__ __forceinline__ bool walk_on(Walk& w, const Params& p, int lane) {
+  __syncwarp();  // every lane is done with this piece
+  if (lane == 0) w.next(p);
+  __syncwarp();
+  return w.more != 0;
+}
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -318,7 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_ready = q_empty + NQT;
   uint64_t* p_ready = s_ready + NQT;
   uint64_t* o_done = p_ready + NQT;
-  uint64_t* x_up = o_done + NQT;
+  uint64_t* s_free = o_done + NQT;   // S_t has been read (own P)
+  uint64_t* pv_done = s_free + NQT;  // P_t V is complete (own P)
+  uint64_t* x_up = pv_done + NQT;
   uint64_t* x_down = x_up + 1;
   uint64_t* drain = x_down + 1;
   CtaCtl* ctl = reinterpret_cast<CtaCtl*>(smem + C::kCtlOff);
@@ -340,6 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_ready[t], 1);
       mbar_init(&p_ready[t], BM);
       mbar_init(&o_done[t], 1);
+      mbar_init(&s_free[t], BM);
+      mbar_init(&pv_done[t], 1);
     }
     mbar_init(x_up, BM);
     mbar_init(x_down, BM);
@@ -364,12 +561,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   grid_wait();  // the plan's writes (and the caller's before it) are visible
   grid_launch_dependents();
-  const long long steps = p.plan.cost[p.B];
-  const int busy = *p.plan.busy;
-  const long long r0 = c < busy ? range_lo(c, steps, busy) : 0;
-  const long long r1 = c < busy ? range_lo(c + 1, steps, busy) : 0;
+  Walk& w = *reinterpret_cast<Walk*>(smem + C::kWalkOff + warp * 80);
+  int chunks;  // CTAs that take a chunk
+  bool work;
+  if (p.inline_plan) {
+    long long* rest_at = reinterpret_cast<long long*>(smem + C::kStgOff);
+    int* chunk_at = reinterpret_cast<int*>(rest_at + p.B + 1);
+    const Head h = make_plan<kThreads>(p, rest_at, chunk_at,
+                                       reinterpret_cast<long long*>(smem + C::kWalkOff), c == 0);
+    chunks = h.chunks;
+    work = c < h.ctas;
+    if (work) {
+      const Start st = plan_find(p, h, rest_at, chunk_at, c, lane);  // (every warp for itself)
+      if (lane == 0) w.start(p, h, st, c);
+      if (threadIdx.x == 0) p.plan.starts[c] = st;  // for the gather, as is the head
+    }
+    if (c == 0 && threadIdx.x == 0) *p.plan.head = h;
+    __syncthreads();  // the scratch is free for the softmax warps
+  } else {
+    const Head h = *p.plan.head;
+    chunks = h.chunks;
+    work = c < h.ctas;
+    if (work && lane == 0) w.start(p, h, p.plan.starts[c], c);
+    __syncwarp();
+  }
 
-  if (r1 <= r0) {
+  if (!work) {
     // nothing for this CTA (uniform over it)
   } else if (warp == kTmaWarp) {
     // ------------------------------------------------------------ producer
@@ -383,8 +600,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t L = 0;        // K/V tiles issued so far (K_j, V_j alternate)
     int qn[NQT] = {0, 0};  // Q loads issued so far, per tile
     bool ok = true;
-    Walk w;
-    w.start(p, c, r1 - r0);
     do {
       const int tiles = w.two(p) ? 2 : 1;
 #pragma unroll
@@ -403,19 +618,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The page that this lane loads of key tile j: its id, or num_pages
       // (out of range: zeros) where the sequence has none.
       const int* row = p.table + static_cast<size_t>(w.b) * p.width;
+      const int keys = w.s.L, g = w.g, n = w.steps();
+      const int j0 = w.lo + w.i0;
+      int at = w.rot;  // step of the piece
       auto page_of = [&](int j) {
         const int key = j * BN + pg * box_rows;
-        if (!loads || key >= w.s.L) return p.num_pages;
+        if (!loads || key >= keys) return p.num_pages;
         const int id = row[key >> p.page_log2];
         if (id >= 0 && id < p.num_pages) return id;
         bad(kBadPage);
         return p.num_pages;
       };
-      int page = page_of(w.lo + w.i0);
-      for (int j = w.lo + w.i0; ok && j < w.lo + w.i1; ++j) {
-        const int y = (j * BN + pg * box_rows) & ((1 << p.page_log2) - 1);
+      int page = page_of(j0 + at);
+      for (int j = 0; ok && j < n; ++j) {
+        const int y = ((j0 + at) * BN + pg * box_rows) & ((1 << p.page_log2) - 1);
         const int now = page;
-        if (j + 1 < w.lo + w.i1) page = page_of(j + 1);  // ahead of its use
+        if (++at == n) at = 0;
+        if (j + 1 < n) page = page_of(j0 + at);  // ahead of its use
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++L) {
           const uint32_t s = L % S, use = L / S;
@@ -426,10 +645,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (loads)
             tma_load_4d(sKV + s * C::kTileBytes + dst_off, kv ? &tm_v : &tm_k, &kv_full[s], bx * 64,
-                        y, w.g, now);
+                        y, g, now);
         }
       }
-    } while (ok && w.next(p));
+    } while (ok && walk_on(w, p, lane));
     // No copy may still be landing in shared memory when the CTA exits.
 #pragma unroll
     for (int t = 0; t < NQT; ++t)
@@ -452,7 +671,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t L = 0;            // K/V tiles consumed before this piece
     int qi[NQT] = {0, 0};      // Q tiles used before this piece
     uint32_t pw[NQT] = {0, 0};  // P tiles used
+    uint32_t sf[NQT] = {0, 0};  // score products issued (own P)
     bool ok = true;
+    // With P in columns of its own, S_t is overwritten when it has been read.
+    auto s_is_free = [&](int t) {
+      if constexpr (C::kOwnP) {
+        if (sf[t] > 0 && !warp_all(wait_bar(&s_free[t], (sf[t] - 1) & 1, ctl, kSiteSFree)))
+          return false;
+        tc_fence_after();
+        ++sf[t];
+      }
+      return true;
+    };
     auto score = [&](int t, int qt, uint32_t lk) {  // S_t = Q_qt K^T
       const uint32_t kd = k_lo + (((lk % S) * C::kTileBytes) >> 4);
       const uint32_t qd = q_lo + ((qt * C::kTileBytes) >> 4);
@@ -469,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto value = [&](int t, uint32_t lv, bool first) {  // O_t (+)= P_t V
       const uint32_t vd = v_lo + (((lv % S) * C::kTileBytes) >> 4);
-      const uint32_t tP = tmem + C::s_col(t) + C::kPCol;
+      const uint32_t tP = tmem + C::p_col(t);
       const uint32_t tO = tmem + C::o_col(t);
       if (first)
         umma_ts_w<0>(tO, tP, desc_words(vd, d_hi), idesc_pv);
@@ -478,13 +708,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int kk = 1; kk < BN / 16; ++kk)
         umma_ts_w<1>(tO, tP + kk * 8, desc_words(vd + kk * 128, d_hi), idesc_pv);
+      if constexpr (C::kOwnP) umma_commit_w(&pv_done[t]);
     };
-    Walk w;
-    w.start(p, c, r1 - r0);
     // Rows of V behind the sequence's last key: zeros (the pages behind it are
     // zeros already; those of its last page may hold anything).
+    int tail = 0, rot = 0, n = 0;  // keys of the sequence from the piece's first key tile on
     auto clear_tail = [&](int j, uint32_t lv) {
-      const int valid = w.s.L - (w.lo + w.i0 + j) * BN;
+      const int valid = tail - (j + rot < n ? j + rot : j + rot - n) * BN;
       if (valid >= BN) return;
       const int from = max(valid, 0);
       uint8_t* base = sKV + (lv % S) * C::kTileBytes;
@@ -498,44 +728,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
     do {
-      const int n = w.steps();
+      n = w.steps();
+      rot = w.rot;
+      tail = w.s.L - (w.lo + w.i0) * BN;
       if (w.two(p)) {
         for (int j = 0; ok && j <= n; ++j) {
           const uint32_t Lk = L + 2 * j, Lv = L + 2 * j - 1;
-          bool have_k = false, have_v = false;
-#pragma unroll
-          for (int t = 0; t < NQT; ++t) {
-            if (!ok) break;
-            if (j >= 1) {
-              if (!have_v) {
-                if (!(ok = warp_all(wait_bar(&kv_full[Lv % S], (Lv / S) & 1, ctl, kSiteKvFull))))
-                  break;
-                have_v = true;
-                clear_tail(j - 1, Lv);
-              }
-              if (!(ok = warp_all(wait_bar(&p_ready[t], pw[t] & 1, ctl, kSitePReady)))) break;
-              ++pw[t];
+          auto scores = [&](int t) {
+            if (j >= n || !ok) return;
+            if (t == 0) {
+              if (!(ok = warp_all(wait_bar(&kv_full[Lk % S], (Lk / S) & 1, ctl, kSiteKvFull)))) return;
               tc_fence_after();
-              value(t, Lv, j == 1);
-              if (j == n) umma_commit_w(&o_done[t]);
             }
-            if (j < n) {
-              if (!have_k) {
-                if (!(ok = warp_all(wait_bar(&kv_full[Lk % S], (Lk / S) & 1, ctl, kSiteKvFull))))
-                  break;
-                tc_fence_after();
-                have_k = true;
-              }
-              if (j == 0) {
-                if (!(ok = warp_all(wait_bar(&q_full[t], qi[t] & 1, ctl, kSiteQFull)))) break;
-                tc_fence_after();
-              }
-              score(t, t, Lk);
-              if (j == n - 1) umma_commit_w(&q_empty[t]);
+            if (j == 0) {
+              if (!(ok = warp_all(wait_bar(&q_full[t], qi[t] & 1, ctl, kSiteQFull)))) return;
+              tc_fence_after();
             }
+            if (!(ok = s_is_free(t))) return;
+            score(t, t, Lk);
+            if (j == n - 1) umma_commit_w(&q_empty[t]);
+            if (t == 1) umma_commit_w(&kv_empty[Lk % S]);
+          };
+          auto values = [&](int t) {
+            if (j < 1 || !ok) return;
+            if (t == 0) {
+              if (!(ok = warp_all(wait_bar(&kv_full[Lv % S], (Lv / S) & 1, ctl, kSiteKvFull)))) return;
+              clear_tail(j - 1, Lv);
+            }
+            if (!(ok = warp_all(wait_bar(&p_ready[t], pw[t] & 1, ctl, kSitePReady)))) return;
+            ++pw[t];
+            tc_fence_after();
+            value(t, Lv, j == 1);
+            if (j == n) umma_commit_w(&o_done[t]);
+            if (t == 1) umma_commit_w(&kv_empty[Lv % S]);
+          };
+          if constexpr (C::kOwnP) {
+            scores(0);
+            scores(1);
+            values(0);
+            values(1);
+          } else {  // S_t goes over P_t: after the product that reads it
+            values(0);
+            scores(0);
+            values(1);
+            scores(1);
           }
-          if (have_k) umma_commit_w(&kv_empty[Lk % S]);
-          if (have_v) umma_commit_w(&kv_empty[Lv % S]);
         }
         ++qi[0];
         ++qi[1];
@@ -549,6 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = warp_all(wait_bar(&kv_full[Lk % S], (Lk / S) & 1, ctl, kSiteKvFull)))) break;
             if (j == 0 && !(ok = warp_all(wait_bar(&q_full[0], qi[0] & 1, ctl, kSiteQFull)))) break;
             tc_fence_after();
+            if (!(ok = s_is_free(j & 1))) break;
             score(j & 1, 0, Lk);
             if (j == n - 1) umma_commit_w(&q_empty[0]);
             umma_commit_w(&kv_empty[Lk % S]);
@@ -569,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++qi[0];
       }
       L += 2 * n;
-    } while (ok && w.next(p));
+    } while (ok && walk_on(w, p, lane));
     // Every MMA must be complete before tensor memory is released.
     umma_commit_w(drain);
     drain_bar(drain, 0, ctl, kSiteDrain);
@@ -579,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q4 = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
     const uint32_t tS = tmem + lane_off + C::s_col(t);
-    const uint32_t tP = tS + C::kPCol;
+    const uint32_t tP = tmem + lane_off + C::p_col(t);
     const uint32_t tO = tmem + lane_off + C::o_col(t);
     uint8_t* stg = smem + C::kStgOff + warp * C::kStgWarpBytes;
     const int r = q4 * 32 + lane;  // row of the tile
@@ -587,27 +825,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t sw = 0;  // s_ready phases consumed
     uint32_t od[NQT] = {0, 0};  // o_done phases (group 0 also follows group 1's in shared pieces)
     uint32_t xp = 0;  // exchanges
+    [[maybe_unused]] uint32_t np = 0;  // P tiles written (own P)
     bool ok = true;
-    Walk w;
-    w.start(p, c, r1 - r0);
     do {
       const int n = w.steps();
       const bool two = w.two(p);
       const int tile = two ? t : 0;                       // tile of rows this group works on
       const int j0 = two ? 0 : t, dj = two ? 1 : 2;       // its key tiles
-      const int tok = (w.pair * NQT + tile) * p.tt + r / p.G;  // this row's token
-      const bool row_ok = r < p.tt * p.G && tok < w.s.T;
+      int pos;  // this row's position (-1 where the row is none, or has no keys)
+      bool row_ok;
+      {
+        const int tok = (w.pair * NQT + tile) * p.tt + r / p.G;  // its token
+        row_ok = r < p.tt * p.G && tok < w.s.T;
+        pos = row_ok ? w.s.L - w.s.T + tok : -1;
+      }
       const bool live = __any_sync(0xffffffffu, row_ok);
-      const int pos = row_ok ? w.s.L - w.s.T + tok : -1;
-      const int kfirst = p.window > 0 ? max(0, pos - p.window + 1) : 0;
       // Key tiles that every row of the tile sees whole need no mask.
       const int base = w.s.L - w.s.T + (w.pair * NQT + tile) * p.tt;
+      const int key0 = (w.lo + w.i0) * BN, rot = w.rot;
       float m = -INFINITY, l = 0.f;
       for (int j = j0; j < n; j += dj) {
         if (!(ok = warp_all(wait_bar(&s_ready[t], sw & 1, ctl, kSiteSReady)))) break;
         ++sw;
         tc_fence_after();
         if (!live) {  // no rows in this warp: its P is never stored
+          if constexpr (C::kOwnP) {
+            mbar_arrive(&s_free[t]);
+            ++np;
+          }
           mbar_arrive(&p_ready[t]);
           continue;
         }
@@ -623,14 +868,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k) s[h * 32 + k] = __uint_as_float(rr[h][k]);
         }
-        const int kv0 = (w.lo + w.i0 + j) * BN;
+        if constexpr (C::kOwnP) {  // S_t read: its columns may take the next scores
+          tc_fence_before();
+          mbar_arrive(&s_free[t]);
+        }
+        const int kv0 = key0 + (j + rot < n ? j + rot : j + rot - n) * BN;
         if (kv0 + BN - 1 > base) {
           const int last = pos - kv0;
 #pragma unroll
           for (int k = 0; k < BN; ++k) s[k] = (k > last) ? -INFINITY : s[k];
         }
         if (p.window > 0 && kv0 < base + p.tt - p.window) {
-          const int first = kfirst - kv0;
+          const int first = pos - p.window + 1 - kv0;
 #pragma unroll
           for (int k = 0; k < BN; ++k) s[k] = (k < first) ? -INFINITY : s[k];
         }
@@ -653,10 +902,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= alpha;
         }
         const float m_use = (m == -INFINITY) ? 0.f : m;
-        l += prefill::exp_tile<T, 0, BN>(s, sl2, m_use, tP);
+        if constexpr (C::kOwnP) {
+          // The first half of P in registers while the previous product may
+          // still read P's columns (and write O).
+          const uint64_t c2 = f2_make(sl2, sl2), nm2 = f2_make(-m_use, -m_use);
+          uint64_t la = f2_make(0.f, 0.f), lb = la;
+          uint32_t pa[32], pb[16];
+          prefill::exp_cols_regs<T, 0, BN, 0, 64>(s, c2, nm2, pa, la, lb);
+          if (np > 0) {
+            if (!(ok = warp_all(wait_bar(&pv_done[t], (np - 1) & 1, ctl, kSitePvDone)))) break;
+            tc_fence_after();
+          }
+          ++np;
+          tmem_st_x16(tP, *reinterpret_cast<uint32_t(*)[16]>(pa));
+          tmem_st_x16(tP + 16, *reinterpret_cast<uint32_t(*)[16]>(pa + 16));
+          prefill::exp_cols_regs<T, 0, BN, 64, 96>(s, c2, nm2, pb, la, lb);
+          tmem_st_x16(tP + 32, pb);
+          prefill::exp_cols_regs<T, 0, BN, 96, 128>(s, c2, nm2, pb, la, lb);
+          tmem_st_x16(tP + 48, pb);
+          float a0, a1, b0, b1;
+          f2_split(la, a0, a1);
+          f2_split(lb, b0, b1);
+          l += (a0 + a1) + (b0 + b1);
+        } else {
+          l += prefill::exp_tile<T, 0, BN>(s, sl2, m_use, tP);
+        }
         if (j > j0 && __any_sync(0xffffffffu, need)) {
-          // O_t was last written by this group's previous product, which
-          // completed before S_t(j) was signalled.
+          // O_t was last written by this group's previous product, complete
+          // before S_t(j) was signalled (own P: waited for above).
 #pragma unroll
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t o[32];
@@ -711,8 +984,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         w1 *= inv;
         const bool whole = w.whole();
         // The row's place: (token, head) in o, or its row in the piece's slot.
-        const int slot = 2 * c + (w.i0 == 0 ? 1 : 0);
-        const size_t prow = static_cast<size_t>(slot) * kSlotRows + tile * BM + r;
+        const size_t prow =
+            static_cast<size_t>(w.slot(c, p.nc, chunks)) * kSlotRows + tile * BM + r;
+        const int tok = (w.pair * NQT + tile) * p.tt + r / p.G;
         const size_t orow = (static_cast<size_t>(w.s.q0) + tok) * p.Hq + w.g * p.G + r % p.G;
         // O, 32 columns at a time through the warp's staging rows, so that a
         // store instruction writes whole lines: 16-byte chunk u of row q sits
@@ -784,7 +1058,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       if (shared) mbar_arrive(x_down);
-    } while (w.next(p));
+    } while (walk_on(w, p, lane));
   }
 
   tc_fence_before();
@@ -796,58 +1070,96 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The items cut between CTAs: block (c, y) folds the one that begins in CTA
-// c's range and goes on in the next ones, rows y, y + gridDim.y * 8, ... of it,
-// one warp per row.
+// The cut items: block (c, y) folds the one whose first chunk is CTA c's, or
+// whose rest begins in CTA c's range and goes on in the next (if it has no
+// chunks), rows 64 y .. 64 y + 63 of its 256, eight a warp. A partial of all
+// eight is loaded before any is used (one at a time it took 27 us for 148 cut
+// items of 256 rows).
 template <typename T>
 __global__ void __launch_bounds__(256) attn_paged_gather_kernel(const Params p) {
+  constexpr int RW = 8;
   grid_wait();
-  const long long steps = p.plan.cost[p.B];
-  const int busy = *p.plan.busy;
+  const Head h = *p.plan.head;
   const int c = blockIdx.x;
-  if (c + 1 >= busy) return;
-  const int4 nx = p.plan.starts[c + 1];
-  const long long r0 = range_lo(c, steps, busy), r1 = range_lo(c + 1, steps, busy);
-  if (nx.w == 0 || nx.w > r1 - r0) return;  // a boundary between items, or begun before c
-  const Seq s = load_seq(p.cu_q, p.lens, nx.x, p.total_q, p.max_q, p.capacity());
-  const Span sp = span_of(p, s, nx.z);
-  const long long end = r1 - nx.w + sp.n;  // one behind the item's last step
-  const int t0 = nx.z * NQT * p.tt;
+  if (c >= h.ctas) return;
+  const bool has_chunks = c < h.chunks;
+  if (!has_chunks && c + 1 >= h.ctas) return;
+  const Start nx = p.plan.starts[has_chunks ? c : c + 1];
+  const Seq s = load_seq(p.cu_q, p.lens, nx.b, p.total_q, p.max_q, p.capacity());
+  const int n = span_of(p, s, nx.pair).n;
+  const int f = chunks_of(n, h.w, h.chunks > 0);
+  const int rest = static_cast<int>(n - f * h.w);
+  if (has_chunks) {
+    if (nx.i != 0 || (f == 1 && rest == 0)) return;  // not the first chunk, or the whole item
+  } else if (f > 0 || nx.i == 0 || nx.i > h.w) {
+    return;  // chunks' business, a boundary between items, or begun before c
+  }
+  // Its partials: chunks c .. c + f - 1, then the CTAs q0 .. q1 of the rest.
+  const int q0 = h.chunks + static_cast<int>(div_pos(nx.rest, h.w));
+  const int q1 = rest > 0 ? h.chunks + static_cast<int>(div_pos(nx.rest + rest - 1, h.w)) : q0 - 1;
+  const int parts = f + q1 - q0 + 1;
+  auto slot_of = [&](int k) {
+    if (k < f) return c + k;
+    if (q0 == q1) return 2 * p.nc + c;
+    return k == f ? p.nc + q0 : q0 + k - f;
+  };
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int rr = blockIdx.y * 8 + warp; rr < kSlotRows; rr += gridDim.y * 8) {
-    const int tile = rr / BM, r = rr - tile * BM;
-    const int tok = t0 + tile * p.tt + r / p.G;
-    if (r >= p.tt * p.G || tok >= s.T) continue;
-    // Partials: slot 2c + 1 of CTA c, then slot 2c' of the CTAs that go on.
-    float mx = -INFINITY, tot = 0.f;
-    float acc[8];  // two pieces of 4 columns: 4 lane, 128 + 4 lane (d <= 128: the first)
+  const int rr0 = blockIdx.y * 64 + warp * RW;  // (one tile: 64 divides 128)
+  const int tile = rr0 / BM, t0 = (nx.pair * NQT + tile) * p.tt;
+  bool have[RW], any = false;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    for (int cc = c; cc < busy && range_lo(cc, steps, busy) < end; ++cc) {
-      const size_t row = static_cast<size_t>(2 * cc + (cc == c ? 1 : 0)) * kSlotRows + rr;
-      const float lse = p.part_lse[row];
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (lane * 4 < p.d) x = *reinterpret_cast<const float4*>(p.part_o + row * p.d + lane * 4);
-      if (lse == -INFINITY) continue;
-      const float nm = fmaxf(mx, lse);
-      const float sc = ex2_approx(mx - nm), wt = ex2_approx(lse - nm);
-      tot = tot * sc + wt;
-      acc[0] = fmaf(wt, x.x, acc[0] * sc);
-      acc[1] = fmaf(wt, x.y, acc[1] * sc);
-      acc[2] = fmaf(wt, x.z, acc[2] * sc);
-      acc[3] = fmaf(wt, x.w, acc[3] * sc);
-      mx = nm;
+  for (int i = 0; i < RW; ++i) {
+    const int r = rr0 + i - tile * BM;
+    have[i] = r < p.tt * p.G && t0 + r / p.G < s.T;
+    any = any || have[i];
+  }
+  if (!any) return;
+  const bool col = lane * 4 < p.d;
+  float mx[RW], tot[RW];
+  float4 acc[RW];
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    mx[i] = -INFINITY;
+    tot[i] = 0.f;
+    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int k = 0; k < parts; ++k) {
+    const size_t row = static_cast<size_t>(slot_of(k)) * kSlotRows + rr0;
+    float lse[RW];
+    float4 x[RW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      lse[i] = have[i] ? p.part_lse[row + i] : -INFINITY;
+      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (have[i] && col) x[i] = *reinterpret_cast<const float4*>(p.part_o + (row + i) * p.d + lane * 4);
     }
-    const float inv = tot > 0.f ? 1.f / tot : 0.f;
-    const size_t orow = (static_cast<size_t>(s.q0) + tok) * p.Hq + nx.y * p.G + r % p.G;
-    if (lane * 4 < p.d) {
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      if (lse[i] == -INFINITY) continue;
+      const float nm = fmaxf(mx[i], lse[i]);
+      const float sc = ex2_approx(mx[i] - nm), wt = ex2_approx(lse[i] - nm);
+      tot[i] = tot[i] * sc + wt;
+      acc[i].x = fmaf(wt, x[i].x, acc[i].x * sc);
+      acc[i].y = fmaf(wt, x[i].y, acc[i].y * sc);
+      acc[i].z = fmaf(wt, x[i].z, acc[i].z * sc);
+      acc[i].w = fmaf(wt, x[i].w, acc[i].w * sc);
+      mx[i] = nm;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    if (!have[i]) continue;
+    const int r = rr0 + i - tile * BM;
+    const float inv = tot[i] > 0.f ? 1.f / tot[i] : 0.f;
+    const size_t orow = (static_cast<size_t>(s.q0) + t0 + r / p.G) * p.Hq + nx.g * p.G + r % p.G;
+    if (col) {
       uint2 v;
-      v.x = prefill::pack2<T>(acc[0] * inv, acc[1] * inv);
-      v.y = prefill::pack2<T>(acc[2] * inv, acc[3] * inv);
+      v.x = prefill::pack2<T>(acc[i].x * inv, acc[i].y * inv);
+      v.y = prefill::pack2<T>(acc[i].z * inv, acc[i].w * inv);
       *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.o) + orow * p.d + lane * 4) = v;
     }
     if (lane == 0 && p.lse != nullptr)
-      p.lse[orow] = tot > 0.f ? (mx + lg2_approx(tot)) * 0.69314718055994531f : -INFINITY;
+      p.lse[orow] = tot[i] > 0.f ? (mx[i] + lg2_approx(tot[i])) * 0.69314718055994531f : -INFINITY;
   }
 }
 
