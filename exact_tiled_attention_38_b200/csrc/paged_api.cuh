@@ -143,8 +143,8 @@ int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap
     rc = launch_dependent(kern, dim3(static_cast<unsigned>(p.nc)), paged::kThreads, smem, st, tq,
                           tk, tv, p);
   if (rc == ATTN_OK)
-    rc = launch_dependent(paged::attn_paged_gather_kernel<T>,
-                          dim3(static_cast<unsigned>(p.nc), 4), 256, 0, st, p);
+    rc = launch_dependent(paged::attn_paged_gather_kernel<D, T>,
+                          dim3(static_cast<unsigned>(p.nc), paged::kSlotRows / 32), 256, 0, st, p);
   return rc;
 }
 
@@ -300,7 +300,7 @@ int paged_run(const void* q, long long q_stride, const attn_pages* pages, const 
   const size_t head = part(sizeof(paged::Head)), starts = part(p.nc * sizeof(paged::Start)),
                rest_at = part(p.inline_plan ? 0 : (static_cast<size_t>(B) + 1) * 8),
                chunk_at = part(p.inline_plan ? 0 : (static_cast<size_t>(B) + 1) * 4),
-               part_lse = part(slots * 4), part_o = part(slots * c.d * 4);
+               part_lse = part(slots * 4), part_o = part(slots * (c.d <= 64 ? 64 : 128) * 4);
   Workspace ws;
   rc = ws.take(end, st);
   if (rc != ATTN_OK) return rc;

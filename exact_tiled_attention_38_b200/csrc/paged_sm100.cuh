@@ -109,7 +109,7 @@ struct Cfg {
   // (m, l) of group 1's rows, where its output would be staged (it stages none then).
   static constexpr int kXOff = kStgOff + 4 * kStgWarpBytes;
   static constexpr int kWalkOff = kCtlOff + 64;  // each warp's way through the range
-  static constexpr int kSmemBytes = kWalkOff + 10 * 80 + 1024;  // + runtime 1024-byte alignment
+  static constexpr int kSmemBytes = kWalkOff + 10 * 96 + 1024;  // + runtime 1024-byte alignment
   static constexpr uint32_t kTmemCols = 512;
   static constexpr bool kOwnP = D == 64;  // P in columns of its own, else over S from column 64 on
   __host__ __device__ static constexpr uint32_t s_col(int t) { return kOwnP ? 256u * t : BN * t; }
@@ -154,7 +154,7 @@ struct Params {
   const int* table;
   void* o;
   float* lse;
-  float* part_o;    // [3 nc][256][d]
+  float* part_o;    // [3 nc] slots of 256 rows: [row / 32][column / 4][row % 32][4]
   float* part_lse;  // [3 nc][256], log2 units
   Plan plan;
   int B, Hq, Hkv, G, tt;
@@ -423,6 +423,9 @@ struct Walk {
   int w;           // steps of a chunk (0: no item has any)
   int left;        // steps of the range behind this piece
   int done;        // and up to its end
+  int chunks;      // CTAs that take a chunk
+  // Softmax warps: phases of their piece-wise barriers used so far.
+  uint32_t od0, od1, xp;
   Seq s;
 
   __device__ __forceinline__ void item(const Params& p) {
@@ -444,6 +447,8 @@ struct Walk {
     const long long rest = h.rest - (c - h.chunks) * h.w;
     left = static_cast<int>(c < h.chunks || rest > h.w ? h.w : rest);
     done = 0;
+    od0 = od1 = xp = 0;
+    chunks = h.chunks;
     more = 1;
     s = load_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
     item(p);
@@ -473,7 +478,7 @@ struct Walk {
   __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == n; }
   // The slot of a piece that is not the whole item, in CTA c of nc: a chunk or
   // what goes on from the CTA before, what goes on in the next, all of a rest.
-  __device__ __forceinline__ int slot(int c, int nc, int chunks) const {
+  __device__ __forceinline__ int slot(int c, int nc) const {
     return c < chunks || i0 != first ? c : i1 < n ? nc + c : 2 * nc + chunk;
   }
   // Both tiles have rows?
@@ -481,7 +486,7 @@ struct Walk {
     return pair * NQT * p.tt + p.tt < s.T;
   }
 };
-static_assert(sizeof(Walk) <= 80, "shared memory of a warp's walk");
+static_assert(sizeof(Walk) <= 96, "shared memory of a warp's walk");
 
 // The warp's walk to its next piece; false at the end of the range.
 __device__ __forceinline__ bool walk_on(Walk& w, const Params& p, int lane) {
@@ -561,15 +566,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   grid_wait();  // the plan's writes (and the caller's before it) are visible
   grid_launch_dependents();
-  Walk& w = *reinterpret_cast<Walk*>(smem + C::kWalkOff + warp * 80);
-  int chunks;  // CTAs that take a chunk
+  Walk& w = *reinterpret_cast<Walk*>(smem + C::kWalkOff + warp * 96);
   bool work;
   if (p.inline_plan) {
     long long* rest_at = reinterpret_cast<long long*>(smem + C::kStgOff);
     int* chunk_at = reinterpret_cast<int*>(rest_at + p.B + 1);
     const Head h = make_plan<kThreads>(p, rest_at, chunk_at,
                                        reinterpret_cast<long long*>(smem + C::kWalkOff), c == 0);
-    chunks = h.chunks;
     work = c < h.ctas;
     if (work) {
       const Start st = plan_find(p, h, rest_at, chunk_at, c, lane);  // (every warp for itself)
@@ -580,7 +583,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();  // the scratch is free for the softmax warps
   } else {
     const Head h = *p.plan.head;
-    chunks = h.chunks;
     work = c < h.ctas;
     if (work && lane == 0) w.start(p, h, p.plan.starts[c], c);
     __syncwarp();
@@ -813,224 +815,229 @@ __global__ void __launch_bounds__(kThreads, 1)
     drain_bar(drain, 0, ctl, kSiteDrain);
   } else {
     // ------------------------------------------------------------ softmax
+    // What a step needs stays in registers beside its 128 scores; everything
+    // of a piece is worked out again from the walk at its end.
     const int t = warp >> 2;
-    const int q4 = warp & 3;
-    const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-    const uint32_t tS = tmem + lane_off + C::s_col(t);
-    const uint32_t tP = tmem + lane_off + C::p_col(t);
-    const uint32_t tO = tmem + lane_off + C::o_col(t);
-    uint8_t* stg = smem + C::kStgOff + warp * C::kStgWarpBytes;
-    const int r = q4 * 32 + lane;  // row of the tile
-    const float sl2 = p.scale_log2;
-    uint32_t sw = 0;  // s_ready phases consumed
-    uint32_t od[NQT] = {0, 0};  // o_done phases (group 0 also follows group 1's in shared pieces)
-    uint32_t xp = 0;  // exchanges
+    uint32_t sw = 0;                   // s_ready phases consumed
     [[maybe_unused]] uint32_t np = 0;  // P tiles written (own P)
     bool ok = true;
     do {
-      const int n = w.steps();
-      const bool two = w.two(p);
-      const int tile = two ? t : 0;                       // tile of rows this group works on
-      const int j0 = two ? 0 : t, dj = two ? 1 : 2;       // its key tiles
-      int pos;  // this row's position (-1 where the row is none, or has no keys)
-      bool row_ok;
-      {
-        const int tok = (w.pair * NQT + tile) * p.tt + r / p.G;  // its token
-        row_ok = r < p.tt * p.G && tok < w.s.T;
-        pos = row_ok ? w.s.L - w.s.T + tok : -1;
-      }
-      const bool live = __any_sync(0xffffffffu, row_ok);
-      // Key tiles that every row of the tile sees whole need no mask.
-      const int base = w.s.L - w.s.T + (w.pair * NQT + tile) * p.tt;
-      const int key0 = (w.lo + w.i0) * BN, rot = w.rot;
       float m = -INFINITY, l = 0.f;
-      for (int j = j0; j < n; j += dj) {
-        if (!(ok = warp_all(wait_bar(&s_ready[t], sw & 1, ctl, kSiteSReady)))) break;
-        ++sw;
-        tc_fence_after();
-        if (!live) {  // no rows in this warp: its P is never stored
-          if constexpr (C::kOwnP) {
-            mbar_arrive(&s_free[t]);
-            ++np;
-          }
-          mbar_arrive(&p_ready[t]);
-          continue;
-        }
-        float s[BN];
+      {
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_off + C::s_col(t);
+        const uint32_t tP = tmem + lane_off + C::p_col(t);
+        const uint32_t tO = tmem + lane_off + C::o_col(t);
+        const float sl2 = p.scale_log2;
+        const bool two = w.two(p);
+        const int tok0 = (w.pair * NQT + (two ? t : 0)) * p.tt;  // first token of the group's tile
+        const int base = w.s.L - w.s.T + tok0;                   // and its position
+        int pos;  // this row's position (-1 where the row is none, or has no keys)
+        bool live;
         {
-          uint32_t rr[BN / 32][32];
-#pragma unroll
-          for (int h = 0; h < BN / 32; ++h) tmem_ld_x32(tS + h * 32, rr[h]);
-#pragma unroll
-          for (int h = 0; h < BN / 32; ++h) tmem_wait_ld_x32(rr[h]);
-#pragma unroll
-          for (int h = 0; h < BN / 32; ++h)
-#pragma unroll
-            for (int k = 0; k < 32; ++k) s[h * 32 + k] = __uint_as_float(rr[h][k]);
+          const int r = (warp & 3) * 32 + lane, tok = tok0 + r / p.G;
+          const bool row_ok = r < p.tt * p.G && tok < w.s.T;
+          pos = row_ok ? w.s.L - w.s.T + tok : -1;
+          live = __any_sync(0xffffffffu, row_ok);
         }
-        if constexpr (C::kOwnP) {  // S_t read: its columns may take the next scores
+        const int kend = (w.lo + w.i1) * BN, kwrap = w.steps() * BN;
+        const int dk = two ? BN : 2 * BN;  // a shared tile's groups take its key tiles in turns
+        int kv0 = (w.lo + w.i0 + w.rot) * BN + (two ? 0 : t * BN);
+        if (kv0 >= kend) kv0 -= kwrap;
+        int left = two ? w.steps() : (w.steps() + 1 - t) >> 1;
+        bool first_step = true;
+        for (; left > 0; --left, first_step = false) {
+          if (!(ok = warp_all(wait_bar(&s_ready[t], sw & 1, ctl, kSiteSReady)))) break;
+          ++sw;
+          tc_fence_after();
+          if (!live) {  // no rows in this warp: its P is never stored
+            if constexpr (C::kOwnP) {
+              mbar_arrive(&s_free[t]);
+              ++np;
+            }
+            mbar_arrive(&p_ready[t]);
+            continue;
+          }
+          float s[BN];
+          {
+            uint32_t rr[BN / 32][32];
+#pragma unroll
+            for (int h = 0; h < BN / 32; ++h) tmem_ld_x32(tS + h * 32, rr[h]);
+#pragma unroll
+            for (int h = 0; h < BN / 32; ++h) tmem_wait_ld_x32(rr[h]);
+#pragma unroll
+            for (int h = 0; h < BN / 32; ++h)
+#pragma unroll
+              for (int k = 0; k < 32; ++k) s[h * 32 + k] = __uint_as_float(rr[h][k]);
+          }
+          if constexpr (C::kOwnP) {  // S_t read: its columns may take the next scores
+            tc_fence_before();
+            mbar_arrive(&s_free[t]);
+          }
+          if (kv0 + BN - 1 > base) {  // not every row sees the whole tile
+            const int last = pos - kv0;
+#pragma unroll
+            for (int k = 0; k < BN; ++k) s[k] = (k > last) ? -INFINITY : s[k];
+          }
+          if (p.window > 0 && kv0 < base + p.tt - p.window) {
+            const int first = pos - p.window + 1 - kv0;
+#pragma unroll
+            for (int k = 0; k < BN; ++k) s[k] = (k < first) ? -INFINITY : s[k];
+          }
+          kv0 += dk;
+          if (kv0 >= kend) kv0 -= kwrap;
+          constexpr int Q = BN / 4;
+          float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[Q], s[Q + 1]);
+          float mx2 = fmaxf(s[2 * Q], s[2 * Q + 1]), mx3 = fmaxf(s[3 * Q], s[3 * Q + 1]);
+#pragma unroll
+          for (int k = 2; k < Q; k += 2) {
+            mx0 = fmax3(mx0, s[k], s[k + 1]);
+            mx1 = fmax3(mx1, s[Q + k], s[Q + k + 1]);
+            mx2 = fmax3(mx2, s[2 * Q + k], s[2 * Q + k + 1]);
+            mx3 = fmax3(mx3, s[3 * Q + k], s[3 * Q + k + 1]);
+          }
+          const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
+          float alpha = 1.f;
+          const bool need = m_tile > m + prefill::kRescaleThreshold;
+          if (need) {
+            alpha = ex2_approx(m - m_tile);  // m = -inf gives 0
+            m = m_tile;
+            l *= alpha;
+          }
+          const float m_use = (m == -INFINITY) ? 0.f : m;
+          if constexpr (C::kOwnP) {
+            // The first half of P in registers while the previous product may
+            // still read P's columns (and write O).
+            const uint64_t c2 = f2_make(sl2, sl2), nm2 = f2_make(-m_use, -m_use);
+            uint64_t la = f2_make(0.f, 0.f), lb = la;
+            uint32_t pa[32], pb[16];
+            prefill::exp_cols_regs<T, 0, BN, 0, 64>(s, c2, nm2, pa, la, lb);
+            if (np > 0) {
+              if (!(ok = warp_all(wait_bar(&pv_done[t], (np - 1) & 1, ctl, kSitePvDone)))) break;
+              tc_fence_after();
+            }
+            ++np;
+            tmem_st_x16(tP, *reinterpret_cast<uint32_t(*)[16]>(pa));
+            tmem_st_x16(tP + 16, *reinterpret_cast<uint32_t(*)[16]>(pa + 16));
+            prefill::exp_cols_regs<T, 0, BN, 64, 96>(s, c2, nm2, pb, la, lb);
+            tmem_st_x16(tP + 32, pb);
+            prefill::exp_cols_regs<T, 0, BN, 96, 128>(s, c2, nm2, pb, la, lb);
+            tmem_st_x16(tP + 48, pb);
+            float a0, a1, b0, b1;
+            f2_split(la, a0, a1);
+            f2_split(lb, b0, b1);
+            l += (a0 + a1) + (b0 + b1);
+          } else {
+            l += prefill::exp_tile<T, 0, BN>(s, sl2, m_use, tP);
+          }
+          if (!first_step && __any_sync(0xffffffffu, need)) {
+            // O_t was last written by this group's previous product, complete
+            // before S_t(j) was signalled (own P: waited for above).
+#pragma unroll
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t o[32];
+              tmem_ld_x32(tO + cc * 32, o);
+              tmem_wait_ld_x32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st_x32(tO + cc * 32, o);
+            }
+          }
+          tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(&s_free[t]);
+          mbar_arrive(&p_ready[t]);
         }
-        const int kv0 = key0 + (j + rot < n ? j + rot : j + rot - n) * BN;
-        if (kv0 + BN - 1 > base) {
-          const int last = pos - kv0;
-#pragma unroll
-          for (int k = 0; k < BN; ++k) s[k] = (k > last) ? -INFINITY : s[k];
-        }
-        if (p.window > 0 && kv0 < base + p.tt - p.window) {
-          const int first = pos - p.window + 1 - kv0;
-#pragma unroll
-          for (int k = 0; k < BN; ++k) s[k] = (k < first) ? -INFINITY : s[k];
-        }
-        constexpr int Q = BN / 4;
-        float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[Q], s[Q + 1]);
-        float mx2 = fmaxf(s[2 * Q], s[2 * Q + 1]), mx3 = fmaxf(s[3 * Q], s[3 * Q + 1]);
-#pragma unroll
-        for (int k = 2; k < Q; k += 2) {
-          mx0 = fmax3(mx0, s[k], s[k + 1]);
-          mx1 = fmax3(mx1, s[Q + k], s[Q + k + 1]);
-          mx2 = fmax3(mx2, s[2 * Q + k], s[2 * Q + k + 1]);
-          mx3 = fmax3(mx3, s[3 * Q + k], s[3 * Q + k + 1]);
-        }
-        const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
-        float alpha = 1.f;
-        const bool need = m_tile > m + prefill::kRescaleThreshold;
-        if (need) {
-          alpha = ex2_approx(m - m_tile);  // m = -inf gives 0
-          m = m_tile;
-          l *= alpha;
-        }
-        const float m_use = (m == -INFINITY) ? 0.f : m;
-        if constexpr (C::kOwnP) {
-          // The first half of P in registers while the previous product may
-          // still read P's columns (and write O).
-          const uint64_t c2 = f2_make(sl2, sl2), nm2 = f2_make(-m_use, -m_use);
-          uint64_t la = f2_make(0.f, 0.f), lb = la;
-          uint32_t pa[32], pb[16];
-          prefill::exp_cols_regs<T, 0, BN, 0, 64>(s, c2, nm2, pa, la, lb);
-          if (np > 0) {
-            if (!(ok = warp_all(wait_bar(&pv_done[t], (np - 1) & 1, ctl, kSitePvDone)))) break;
-            tc_fence_after();
-          }
-          ++np;
-          tmem_st_x16(tP, *reinterpret_cast<uint32_t(*)[16]>(pa));
-          tmem_st_x16(tP + 16, *reinterpret_cast<uint32_t(*)[16]>(pa + 16));
-          prefill::exp_cols_regs<T, 0, BN, 64, 96>(s, c2, nm2, pb, la, lb);
-          tmem_st_x16(tP + 32, pb);
-          prefill::exp_cols_regs<T, 0, BN, 96, 128>(s, c2, nm2, pb, la, lb);
-          tmem_st_x16(tP + 48, pb);
-          float a0, a1, b0, b1;
-          f2_split(la, a0, a1);
-          f2_split(lb, b0, b1);
-          l += (a0 + a1) + (b0 + b1);
-        } else {
-          l += prefill::exp_tile<T, 0, BN>(s, sl2, m_use, tP);
-        }
-        if (j > j0 && __any_sync(0xffffffffu, need)) {
-          // O_t was last written by this group's previous product, complete
-          // before S_t(j) was signalled (own P: waited for above).
-#pragma unroll
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t o[32];
-            tmem_ld_x32(tO + cc * 32, o);
-            tmem_wait_ld_x32(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st_x32(tO + cc * 32, o);
-          }
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&p_ready[t]);
       }
       if (!ok) break;
 
       // ---- end of a piece
-      const bool shared = !two && n > 1;  // group 1 has a part of the same rows
-      float w0 = 1.f, w1 = 0.f;           // weights of O_0 and O_1
+      const bool two = w.two(p);
+      const bool shared = !two && w.steps() > 1;  // group 1 has a part of the same rows
+      const int r = (warp & 3) * 32 + lane;       // row of the tile
       if (!two && t == 1) {
         if (shared) {
           // Hand (m, l) to group 0 and wait until it has read O_1.
           xrow[r] = make_float2(m, l);
           mbar_arrive(x_up);
-          ok = warp_all(wait_bar(x_down, xp & 1, ctl, kSiteXDown));
-          ++xp;
-          ++od[1];  // (group 0 waited for it)
+          ok = warp_all(wait_bar(x_down, w.xp & 1, ctl, kSiteXDown));
+          __syncwarp();
+          if (lane == 0) {
+            ++w.xp;
+            ++w.od1;  // (group 0 waited for it)
+          }
           if (!ok) break;
         }
         continue;
       }
-      if (!(ok = warp_all(wait_bar(&o_done[t], od[t] & 1, ctl, kSiteODone)))) break;
-      ++od[t];
+      if (!(ok = warp_all(wait_bar(&o_done[t], (t ? w.od1 : w.od0) & 1, ctl, kSiteODone)))) break;
+      float w0 = 1.f, w1 = 0.f;  // weights of O_0 and O_1
       if (shared) {
-        if (!(ok = warp_all(wait_bar(&o_done[1], od[1] & 1, ctl, kSiteODone)))) break;
-        ++od[1];
-        if (!(ok = warp_all(wait_bar(x_up, xp & 1, ctl, kSiteXUp)))) break;
-        ++xp;
+        if (!(ok = warp_all(wait_bar(&o_done[1], w.od1 & 1, ctl, kSiteODone)))) break;
+        if (!(ok = warp_all(wait_bar(x_up, w.xp & 1, ctl, kSiteXUp)))) break;
         const float2 other = xrow[r];
         const float mm = fmaxf(m, other.x);
         w0 = m == -INFINITY ? 0.f : ex2_approx(m - mm);
         w1 = other.x == -INFINITY ? 0.f : ex2_approx(other.x - mm);
         l = l * w0 + other.y * w1;
         m = mm;
-      } else if (t == 0 && two) {
-        ++od[1];  // group 1 waits for its own; keep count of its phases
+      }
+      __syncwarp();
+      if (lane == 0) {  // (each group keeps count of the other's phases too)
+        if (two || t == 0) ++w.od0;
+        if (two || shared) ++w.od1;
+        if (shared) ++w.xp;
       }
       tc_fence_after();
-      if (live) {
+      const int tile = two ? t : 0, tok = (w.pair * NQT + tile) * p.tt + r / p.G;
+      const bool row_ok = r < p.tt * p.G && tok < w.s.T;
+      if (__any_sync(0xffffffffu, row_ok)) {
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         w0 *= inv;
         w1 *= inv;
-        const bool whole = w.whole();
-        // The row's place: (token, head) in o, or its row in the piece's slot.
-        const size_t prow =
-            static_cast<size_t>(w.slot(c, p.nc, chunks)) * kSlotRows + tile * BM + r;
-        const int tok = (w.pair * NQT + tile) * p.tt + r / p.G;
-        const size_t orow = (static_cast<size_t>(w.s.q0) + tok) * p.Hq + w.g * p.G + r % p.G;
-        // O, 32 columns at a time through the warp's staging rows, so that a
-        // store instruction writes whole lines: 16-byte chunk u of row q sits
-        // at chunk u ^ (q % 8).
-        const long long my = row_ok ? static_cast<long long>(whole ? orow : prow) : -1;
+        // 32 columns of the row's O, normalised; zeros for a row without keys
+        // (O may hold anything).
+        auto columns = [&](int col, float (&f)[32]) {
+          uint32_t o[32];
+          tmem_ld_x32(tmem + lane_off + C::o_col(t) + col, o);
+          tmem_wait_ld_x32(o);
 #pragma unroll
-        for (int half = 0; half < D / 64; ++half) {
-          float f[64];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t o[32];
-            tmem_ld_x32(tO + half * 64 + h * 32, o);
+          for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * w0;
+          if (shared) {
+            tmem_ld_x32(tmem + lane_off + C::o_col(1) + col, o);
             tmem_wait_ld_x32(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) f[h * 32 + e] = __uint_as_float(o[e]) * w0;
-            if (shared) {
-              tmem_ld_x32(tmem + lane_off + C::o_col(1) + half * 64 + h * 32, o);
-              tmem_wait_ld_x32(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) f[h * 32 + e] = fmaf(__uint_as_float(o[e]), w1, f[h * 32 + e]);
-            }
+            for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), w1, f[e]);
           }
-          if (l <= 0.f) {  // no visible key: O may hold anything
+          if (l <= 0.f) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e) f[e] = 0.f;
+            for (int e = 0; e < 32; ++e) f[e] = 0.f;
           }
-          // whole: 64 columns of T are one staged line; partial: two of fp32.
-          for (int h = 0; h < (whole ? 1 : 2); ++h) {
+        };
+        const float l2 = l > 0.f ? m + lg2_approx(l) : -INFINITY;
+        if (w.whole()) {
+          // 64 columns at a time through the warp's staging rows, so that a
+          // store instruction writes whole lines: 16-byte chunk u of row q
+          // sits at chunk u ^ (q % 8).
+          uint8_t* stg = smem + C::kStgOff + warp * C::kStgWarpBytes;
+          const size_t orow = (static_cast<size_t>(w.s.q0) + tok) * p.Hq + w.g * p.G + r % p.G;
+          const long long my = row_ok ? static_cast<long long>(orow) : -1;
+#pragma unroll
+          for (int half = 0; half < D / 64; ++half) {
             __syncwarp();
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              uint4 v;
-              if (whole) {
+            for (int h = 0; h < 2; ++h) {
+              float f[32];
+              columns(half * 64 + h * 32, f);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                uint4 v;
                 v.x = prefill::pack2<T>(f[8 * u], f[8 * u + 1]);
                 v.y = prefill::pack2<T>(f[8 * u + 2], f[8 * u + 3]);
                 v.z = prefill::pack2<T>(f[8 * u + 4], f[8 * u + 5]);
                 v.w = prefill::pack2<T>(f[8 * u + 6], f[8 * u + 7]);
-              } else {
-                v.x = __float_as_uint(h ? f[32 + 4 * u] : f[4 * u]);
-                v.y = __float_as_uint(h ? f[33 + 4 * u] : f[4 * u + 1]);
-                v.z = __float_as_uint(h ? f[34 + 4 * u] : f[4 * u + 2]);
-                v.w = __float_as_uint(h ? f[35 + 4 * u] : f[4 * u + 3]);
+                *reinterpret_cast<uint4*>(stg + lane * 128 + (((h * 4 + u) ^ (lane & 7)) << 4)) = v;
               }
-              *reinterpret_cast<uint4*>(stg + lane * 128 + ((u ^ (lane & 7)) << 4)) = v;
             }
             __syncwarp();
 #pragma unroll
@@ -1038,22 +1045,29 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int q = k * 4 + (lane >> 3), u = lane & 7;
               const long long to = __shfl_sync(0xffffffffu, my, q);
               const uint4 v = *reinterpret_cast<const uint4*>(stg + q * 128 + ((u ^ (q & 7)) << 4));
-              const int col = whole ? half * 64 + u * 8 : half * 64 + h * 32 + u * 4;
-              if (to >= 0 && col < p.d) {
-                if (whole)
-                  *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.o) + to * p.d + col) = v;
-                else
-                  *reinterpret_cast<uint4*>(p.part_o + to * p.d + col) = v;
-              }
+              const int col = half * 64 + u * 8;
+              if (to >= 0 && col < p.d)
+                *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.o) + to * p.d + col) = v;
             }
           }
-        }
-        if (row_ok) {
-          const float l2 = l > 0.f ? m + lg2_approx(l) : -INFINITY;
-          if (!whole)
-            p.part_lse[prow] = l2;
-          else if (p.lse != nullptr)
-            p.lse[orow] = l2 * 0.69314718055994531f;
+          if (row_ok && p.lse != nullptr) p.lse[orow] = l2 * 0.69314718055994531f;
+        } else {
+          // A partial, 32 rows of the slot per warp: columns 4u .. 4u + 3 of
+          // all rows side by side, so that what a thread holds goes out in
+          // whole lines as it is.
+          const size_t rows32 = static_cast<size_t>(w.slot(c, p.nc)) * (kSlotRows / 32) +
+                                (tile * BM + (warp & 3) * 32) / 32;
+          float4* dst = reinterpret_cast<float4*>(p.part_o) + rows32 * (8 * D) + lane;
+#pragma unroll
+          for (int col = 0; col < D; col += 32) {
+            float f[32];
+            columns(col, f);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              dst[(col / 4 + u) * 32] =
+                  make_float4(f[4 * u], f[4 * u + 1], f[4 * u + 2], f[4 * u + 3]);
+          }
+          p.part_lse[rows32 * 32 + lane] = row_ok ? l2 : -INFINITY;
         }
       }
       tc_fence_before();
@@ -1072,12 +1086,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The cut items: block (c, y) folds the one whose first chunk is CTA c's, or
 // whose rest begins in CTA c's range and goes on in the next (if it has no
-// chunks), rows 64 y .. 64 y + 63 of its 256, eight a warp. A partial of all
-// eight is loaded before any is used (one at a time it took 27 us for 148 cut
-// items of 256 rows).
-template <typename T>
+// chunks), rows 32 y .. 32 y + 31 of its 256: lane = row, warp w takes columns
+// 4 (w + 8 k). All of a partial's columns are loaded before any is used, and
+// the result goes out through shared memory in whole lines. (One row a warp at
+// a time, partials in rows, this took 27 us for 148 cut items of 256 rows.)
+template <int D, typename T>
 __global__ void __launch_bounds__(256) attn_paged_gather_kernel(const Params p) {
-  constexpr int RW = 8;
+  constexpr int CW = D / 32;  // 4-column units of a thread
+  __shared__ __align__(16) uint8_t stage[32 * (2 * D + 16)];
   grid_wait();
   const Head h = *p.plan.head;
   const int c = blockIdx.x;
@@ -1086,6 +1102,9 @@ __global__ void __launch_bounds__(256) attn_paged_gather_kernel(const Params p) 
   if (!has_chunks && c + 1 >= h.ctas) return;
   const Start nx = p.plan.starts[has_chunks ? c : c + 1];
   const Seq s = load_seq(p.cu_q, p.lens, nx.b, p.total_q, p.max_q, p.capacity());
+  const int tile = blockIdx.y / 4, t0 = (nx.pair * NQT + tile) * p.tt;
+  const int r0 = (blockIdx.y & 3) * 32;  // rows r0 .. r0 + 31 of the tile
+  if (r0 >= p.tt * p.G || t0 + r0 / p.G >= s.T) return;  // none
   const int n = span_of(p, s, nx.pair).n;
   const int f = chunks_of(n, h.w, h.chunks > 0);
   const int rest = static_cast<int>(n - f * h.w);
@@ -1104,62 +1123,53 @@ __global__ void __launch_bounds__(256) attn_paged_gather_kernel(const Params p) 
     return k == f ? p.nc + q0 : q0 + k - f;
   };
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rr0 = blockIdx.y * 64 + warp * RW;  // (one tile: 64 divides 128)
-  const int tile = rr0 / BM, t0 = (nx.pair * NQT + tile) * p.tt;
-  bool have[RW], any = false;
+  float mx = -INFINITY, tot = 0.f;
+  float4 acc[CW];
 #pragma unroll
-  for (int i = 0; i < RW; ++i) {
-    const int r = rr0 + i - tile * BM;
-    have[i] = r < p.tt * p.G && t0 + r / p.G < s.T;
-    any = any || have[i];
-  }
-  if (!any) return;
-  const bool col = lane * 4 < p.d;
-  float mx[RW], tot[RW];
-  float4 acc[RW];
-#pragma unroll
-  for (int i = 0; i < RW; ++i) {
-    mx[i] = -INFINITY;
-    tot[i] = 0.f;
-    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+  for (int u = 0; u < CW; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
   for (int k = 0; k < parts; ++k) {
-    const size_t row = static_cast<size_t>(slot_of(k)) * kSlotRows + rr0;
-    float lse[RW];
-    float4 x[RW];
+    const size_t rows32 = static_cast<size_t>(slot_of(k)) * (kSlotRows / 32) + blockIdx.y;
+    const float lse = p.part_lse[rows32 * 32 + lane];
+    const float4* src = reinterpret_cast<const float4*>(p.part_o) + rows32 * (8 * D) + lane;
+    float4 x[CW];
 #pragma unroll
-    for (int i = 0; i < RW; ++i) {
-      lse[i] = have[i] ? p.part_lse[row + i] : -INFINITY;
-      x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (have[i] && col) x[i] = *reinterpret_cast<const float4*>(p.part_o + (row + i) * p.d + lane * 4);
-    }
+    for (int u = 0; u < CW; ++u) x[u] = src[(warp + 8 * u) * 32];
+    if (lse == -INFINITY) continue;
+    const float nm = fmaxf(mx, lse);
+    const float sc = ex2_approx(mx - nm), wt = ex2_approx(lse - nm);
+    tot = tot * sc + wt;
 #pragma unroll
-    for (int i = 0; i < RW; ++i) {
-      if (lse[i] == -INFINITY) continue;
-      const float nm = fmaxf(mx[i], lse[i]);
-      const float sc = ex2_approx(mx[i] - nm), wt = ex2_approx(lse[i] - nm);
-      tot[i] = tot[i] * sc + wt;
-      acc[i].x = fmaf(wt, x[i].x, acc[i].x * sc);
-      acc[i].y = fmaf(wt, x[i].y, acc[i].y * sc);
-      acc[i].z = fmaf(wt, x[i].z, acc[i].z * sc);
-      acc[i].w = fmaf(wt, x[i].w, acc[i].w * sc);
-      mx[i] = nm;
+    for (int u = 0; u < CW; ++u) {
+      acc[u].x = fmaf(wt, x[u].x, acc[u].x * sc);
+      acc[u].y = fmaf(wt, x[u].y, acc[u].y * sc);
+      acc[u].z = fmaf(wt, x[u].z, acc[u].z * sc);
+      acc[u].w = fmaf(wt, x[u].w, acc[u].w * sc);
     }
+    mx = nm;
   }
+  const float inv = tot > 0.f ? 1.f / tot : 0.f;
 #pragma unroll
-  for (int i = 0; i < RW; ++i) {
-    if (!have[i]) continue;
-    const int r = rr0 + i - tile * BM;
-    const float inv = tot[i] > 0.f ? 1.f / tot[i] : 0.f;
-    const size_t orow = (static_cast<size_t>(s.q0) + t0 + r / p.G) * p.Hq + nx.g * p.G + r % p.G;
-    if (col) {
-      uint2 v;
-      v.x = prefill::pack2<T>(acc[i].x * inv, acc[i].y * inv);
-      v.y = prefill::pack2<T>(acc[i].z * inv, acc[i].w * inv);
-      *reinterpret_cast<uint2*>(reinterpret_cast<T*>(p.o) + orow * p.d + lane * 4) = v;
-    }
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[orow] = tot[i] > 0.f ? (mx[i] + lg2_approx(tot[i])) * 0.69314718055994531f : -INFINITY;
+  for (int u = 0; u < CW; ++u) {
+    uint2 v;
+    v.x = prefill::pack2<T>(acc[u].x * inv, acc[u].y * inv);
+    v.y = prefill::pack2<T>(acc[u].z * inv, acc[u].w * inv);
+    *reinterpret_cast<uint2*>(stage + lane * (2 * D + 16) + (warp + 8 * u) * 8) = v;
+  }
+  auto out_row = [&](int q, long long& orow) {  // row q of the 32: is there one, and where
+    const int r = r0 + q, tok = t0 + r / p.G;
+    orow = (static_cast<long long>(s.q0) + tok) * p.Hq + nx.g * p.G + r % p.G;
+    return r < p.tt * p.G && tok < s.T;
+  };
+  long long orow;
+  if (warp == 0 && p.lse != nullptr && out_row(lane, orow))
+    p.lse[orow] = tot > 0.f ? (mx + lg2_approx(tot)) * 0.69314718055994531f : -INFINITY;
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * D / 8; i += 256) {
+    const int q = i / (D / 8), u = i % (D / 8);
+    if (u * 8 < p.d && out_row(q, orow))
+      *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.o) + orow * p.d + u * 8) =
+          *reinterpret_cast<const uint4*>(stage + q * (2 * D + 16) + u * 16);
   }
 }
 
