@@ -1,13 +1,17 @@
-"""Build the CUDA library in-tree: ``libattn.so`` next to this file.
+"""Build the CUDA library in-tree: ``libattn.so`` next to this file, and the
+compiled part of the Python binding, ``_binding.so`` (where torch is installed,
+whose tensors it takes; the library itself needs neither).
 
 Compiled for sm_100a only (B200). Usage: ``python -m exact_tiled_attention_38_b200.build``.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -19,6 +23,10 @@ DEPS = sorted(
     for f in os.listdir(os.path.join(PKG_DIR, "csrc"))
     if f.endswith((".cu", ".cuh", ".h"))
 ) + [os.path.join(ROOT, "include", "attn.h")]
+
+BINDING_SRC = os.path.join(PKG_DIR, "csrc", "binding.cpp")
+BINDING_OUT = os.path.join(PKG_DIR, "_binding.so")
+BINDING_DEPS = [BINDING_SRC, os.path.join(ROOT, "include", "attn.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -34,14 +42,40 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(OUT):
+def up_to_date(out: str = OUT, deps=None) -> bool:
+    if not os.path.exists(out):
         return False
-    t = os.path.getmtime(OUT)
-    return all(os.path.getmtime(d) <= t for d in DEPS)
+    t = os.path.getmtime(out)
+    return all(os.path.getmtime(d) <= t for d in (DEPS if deps is None else deps))
+
+
+def build_binding(force: bool = False, verbose: bool = False):
+    """``_binding.so`` against the installed torch; None where there is none."""
+    if not force and up_to_date(BINDING_OUT, BINDING_DEPS):
+        return BINDING_OUT
+    spec = importlib.util.find_spec("torch")  # (found, not imported)
+    if spec is None:
+        return None
+    torch = list(spec.submodule_search_locations)[0]
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    inc = os.path.join(torch, "include")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           "-D_GLIBCXX_USE_CXX11_ABI=1", "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-o", BINDING_OUT + ".tmp", BINDING_SRC, "-L", os.path.join(torch, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    os.replace(BINDING_OUT + ".tmp", BINDING_OUT)
+    return BINDING_OUT
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_binding(force, verbose)
     if not force and up_to_date():
         return OUT
     cmd = [nvcc_path(), *NVCC_FLAGS, "-o", OUT + ".tmp", SRC]
