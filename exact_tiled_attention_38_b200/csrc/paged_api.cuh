@@ -346,13 +346,11 @@ int launch_rope(rope::Params p, int interleaved, cudaStream_t st) {
   if (ny > 65535) return ATTN_ERR_INVALID;
   const dim3 grid(static_cast<unsigned>(blocks_x), static_cast<unsigned>(ny));
   const int smem = tokens * (p.rot / 2) * 8;
-  if (vec)
-    interleaved ? rope::rope_kernel<T, APPEND, true, true><<<grid, rope::kThreads, smem, st>>>(p)
-                : rope::rope_kernel<T, APPEND, false, true><<<grid, rope::kThreads, smem, st>>>(p);
-  else
-    interleaved ? rope::rope_kernel<T, APPEND, true, false><<<grid, rope::kThreads, smem, st>>>(p)
-                : rope::rope_kernel<T, APPEND, false, false><<<grid, rope::kThreads, smem, st>>>(p);
-  return launch_status();
+  const auto kern = vec ? (interleaved ? rope::rope_kernel<T, APPEND, true, true>
+                                       : rope::rope_kernel<T, APPEND, false, true>)
+                        : (interleaved ? rope::rope_kernel<T, APPEND, true, false>
+                                       : rope::rope_kernel<T, APPEND, false, false>);
+  return launch_dependent(kern, grid, rope::kThreads, smem, st, p);
 }
 
 template <typename T>
@@ -489,8 +487,26 @@ inline int pages_setup(const attn_pages* c, int layers, long long layer_stride, 
   return ATTN_OK;
 }
 
-template <typename K>
-int pages_launch(K kern, pages::Params p, pages::CopyParams cp, cudaStream_t st) {
+// One CTA settles the whole numbers when the counts fit its shared memory and
+// the tables have few entries, which it reads and writes alone.
+#ifndef ETA_PAGES_SMALL_ENTRIES
+#define ETA_PAGES_SMALL_ENTRIES 65536
+#endif
+constexpr size_t kPagesSmallBytes = 200 * 1024;
+
+template <void (*kern)(pages::Params)>
+int pages_launch_small(const pages::Params& p, size_t words, cudaStream_t st) {
+  static PerDeviceOnce attr;  // (one for each kernel)
+  const cudaError_t e = attr.run([&]() {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kPagesSmallBytes));
+  });
+  if (e != cudaSuccess) return cuda_fail(e);
+  return launch_dependent(kern, dim3(1), pages::kThreads, static_cast<int>(words * 4), st, p);
+}
+
+template <bool UPDATE>
+int pages_launch(pages::Params p, pages::CopyParams cp, cudaStream_t st) {
   DeviceInfo dev;
   if (device_info(&dev) != ATTN_OK) return ATTN_ERR_CUDA;
   if (!dev.sm100) return ATTN_ERR_UNSUPPORTED;
@@ -518,8 +534,17 @@ int pages_launch(K kern, pages::Params p, pages::CopyParams cp, cudaStream_t st)
   cp.from = p.from;
   cp.to = p.to;
   cp.n_copies = p.n_copies;
-  kern<<<pages::kCtas, pages::kThreads, 0, st>>>(p);
-  rc = launch_status();
+  const size_t words = UPDATE ? pages::update_small_words(p.B, p.P) : pages::compact_small_words(p.P);
+  const bool small = words * 4 <= kPagesSmallBytes &&
+                     static_cast<long long>(p.B) * p.width <= ETA_PAGES_SMALL_ENTRIES;
+  if constexpr (UPDATE)
+    rc = small ? pages_launch_small<pages::pages_update_small_kernel>(p, words, st)
+               : launch_dependent(pages::pages_update_kernel, dim3(pages::kCtas), pages::kThreads, 0,
+                                  st, p);
+  else
+    rc = small ? pages_launch_small<pages::pages_compact_small_kernel>(p, words, st)
+               : launch_dependent(pages::pages_compact_kernel, dim3(pages::kCtas), pages::kThreads, 0,
+                                  st, p);
   if (rc == ATTN_OK)
     rc = launch_dependent(pages::pages_copy_kernel, dim3(static_cast<unsigned>(6 * dev.sm_count)),
                           pages::kCopyThreads, 0, st, cp);
@@ -542,7 +567,7 @@ int pages_update(const attn_pages* c, int layers, long long layer_stride, const 
   p.source = source;
   p.add = add;
   p.lens_out = lens_out;
-  return pages_launch(pages::pages_update_kernel, p, cp, st);
+  return pages_launch<true>(p, cp, st);
 }
 
 int pages_compact(const attn_pages* c, int layers, long long layer_stride, const int32_t* lens,
@@ -554,7 +579,7 @@ int pages_compact(const attn_pages* c, int layers, long long layer_stride, const
   const int rc = pages_setup(c, layers, layer_stride, B, lens, refs, table_out, refs_out, info,
                              &cache, &p, &cp);
   if (rc != ATTN_OK) return rc;
-  return pages_launch(pages::pages_compact_kernel, p, cp, st);
+  return pages_launch<false>(p, cp, st);
 }
 
 // Turns per position of each pair, in 64 bits, on the host.

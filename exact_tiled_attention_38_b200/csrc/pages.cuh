@@ -1,8 +1,10 @@
 // Page operations of a paged cache: rows taking over other rows (forks, beam
 // steps, ended and new sequences) and growing, and compaction of the live
 // pages. Both first settle the whole numbers (block tables, reference counts,
-// which page goes where) in one cluster of CTAs, whose hardware barrier stands
-// between the steps, then copy page contents with the whole grid.
+// which page goes where), then copy page contents with the whole grid. The
+// whole numbers are one CTA's work when the counts fit its shared memory and
+// the tables are not large, else a cluster's, whose hardware barrier stands
+// between the steps.
 //
 // Free pages are those with a reference count <= 0, and are always taken
 // lowest first in the order of the rows, so the result does not depend on
@@ -18,9 +20,8 @@
 // and written, so the copies need no order among them.
 //
 // Bound: the whole numbers by latency (a few dependent passes over the tables
-// and the counts, which stay in L2), the contents by memory (each moved page is
-// read once and written once). One cluster of 8 CTAs keeps the steps in one
-// launch; a barrier of its CTAs costs about a microsecond.
+// and the counts), the contents by memory (each moved page is read once and
+// written once).
 #pragma once
 
 #include <climits>
@@ -146,6 +147,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   const int rank = cta_rank(), tid = threadIdx.x;
   const int all = kCtas * kThreads, me = rank * kThreads + tid;
   const int lane = tid & 31, wid = me >> 5, warps = all >> 5;
+  paged::grid_wait();
   paged::grid_launch_dependents();
 
   // 1. The outputs start as the inputs; no row keeps a last page yet.
@@ -275,6 +277,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   const int rank = cta_rank(), tid = threadIdx.x;
   const int all = kCtas * kThreads, me = rank * kThreads + tid;
   const int lane = tid & 31, wid = me >> 5, warps = all >> 5;
+  paged::grid_wait();
   paged::grid_launch_dependents();
 
   // 1. Live pages of each thread's share of the pool.
@@ -339,6 +342,235 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
+// ------------------------------------------------------------------ one CTA
+// The same two operations by one CTA with the counts in its shared memory.
+
+// Words of dynamic shared memory.
+inline size_t update_small_words(int B, int P) { return 2 * static_cast<size_t>(P) + 7 * static_cast<size_t>(B) + 1; }
+inline size_t compact_small_words(int P) { return 2 * static_cast<size_t>(P); }
+
+// Calls f(i, rank) for the entries i of [0, n) where pick(i) holds, rank being
+// their number in order; returns how many there are. A warp takes a contiguous
+// share, 32 entries at a time. `red` holds 33 words.
+template <typename Pick, typename F>
+__device__ __forceinline__ int each_in_order(int n, int* red, Pick pick, F f) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int share = (n + kThreads - 1) / kThreads * 32;
+  const int i0 = min(n, warp * share), i1 = min(n, i0 + share);
+  int mine = 0;
+  for (int i = i0 + lane; i - lane < i1; i += 32)
+    mine += __popc(__ballot_sync(0xffffffffu, i < i1 && pick(i)));
+  __syncthreads();  // red's last use
+  if (lane == 0) red[warp] = mine;
+  __syncthreads();
+  const int v = red[lane];
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  int at = __shfl_sync(0xffffffffu, x - v, warp);
+  const int all = __shfl_sync(0xffffffffu, x, 31);
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    const bool p = i < i1 && pick(i);
+    const unsigned m = __ballot_sync(0xffffffffu, p);
+    if (p) f(i, at + __popc(m & ((1u << lane) - 1)));
+    at += __popc(m);
+  }
+  return all;
+}
+
+// A row of s tokens' worth that k rows go on from: its full pages' counts
+// change by k - 1, its last, partly filled page's by -1 if k = 0. Rows that
+// just go on (k = 1) need not be read for that.
+__global__ void __launch_bounds__(kThreads, 1) pages_update_small_kernel(const Params p) {
+  extern __shared__ int sm[];
+  __shared__ int red[33];
+  __shared__ int s_copies, s_long;
+  int* refs = sm;               // [P]
+  int* list = refs + p.P;       // [P] free pages in order
+  int* len = list + p.P;        // [B]
+  int* src = len + p.B;         // [B]
+  int* longer = src + p.B;      // [B]
+  int* keeper = longer + p.B;   // [B]
+  int* takers = keeper + p.B;   // [B]
+  int* kept = takers + p.B;     // [B]
+  int* first = kept + p.B;      // [B + 1] fresh pages before each row
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  paged::grid_wait();
+  paged::grid_launch_dependents();
+
+  for (int b = tid; b < p.B; b += kThreads) {
+    const int l = p.lens[b], L = clamp_len(l, p), s = p.source[b];
+    if (l > L) paged::bad(paged::kBadLength);
+    if (s < -1 || s >= p.B) paged::bad(paged::kBadSource);
+    len[b] = L;
+    src[b] = s >= 0 && s < p.B ? s : -1;
+    longer[b] = max(p.add[b], 0);  // (with the source's tokens below)
+    keeper[b] = INT_MAX;
+    takers[b] = 0;
+  }
+#pragma unroll 4
+  for (int i = tid; i < p.P; i += kThreads) refs[i] = p.refs[i];
+  if (tid == 0) s_copies = s_long = 0;
+  __syncthreads();
+
+  for (int b = tid; b < p.B; b += kThreads) {
+    const int s = src[b];
+    if (s < 0) continue;
+    atomicAdd(takers + s, 1);
+    atomicMin(keeper + s, s == b ? -1 : b);
+  }
+  __syncthreads();
+
+  for (int b = warp; b < p.B; b += kThreads / 32) {
+    const int k = takers[b];
+    if (k == 1) continue;
+    const int full = len[b] >> p.page_log2, held = ceil_pages(len[b], p.page_log2);
+    for (int j = lane; j < held; j += 32) {
+      const int d = j < full ? k - 1 : k > 0 ? 0 : -1;
+      const int page = p.table[static_cast<size_t>(b) * p.width + j];
+      if (page < 0 || page >= p.P)
+        paged::bad(paged::kBadPage);
+      else if (d != 0)
+        atomicAdd(refs + page, d);
+    }
+  }
+  // What each row keeps and needs, a few rows a thread.
+  const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  int sum = 0, need;
+  for (int b = b0; b < b1; ++b) {
+    const int s = src[b], L = s >= 0 ? len[s] : 0;
+    const bool keeps = s >= 0 && keeper[s] == (s == b ? -1 : b);
+    kept[b] = keeps ? ceil_pages(L, p.page_log2) : L >> p.page_log2;
+    const long long n = static_cast<long long>(L) + longer[b];
+    longer[b] = static_cast<int>(min(n, static_cast<long long>(INT_MAX)));
+    const int want = ceil_pages(longer[b], p.page_log2);
+    if (want > p.width)
+      atomicAdd(&s_long, 1);
+    else
+      sum += want - kept[b];
+  }
+  int run = block_scan(sum, red, &need);
+  for (int b = b0; b < b1; ++b) {
+    first[b] = run;
+    const int want = ceil_pages(longer[b], p.page_log2);
+    if (want <= p.width) run += want - kept[b];
+  }
+  __syncthreads();
+  const int n_free = each_in_order(
+      p.P, red, [&](int i) { return refs[i] <= 0; },
+      [&](int i, int k) {
+        if (k < need) list[k] = i;
+      });
+  const bool refused = need > n_free || s_long > 0;
+  __syncthreads();
+
+  for (int b = warp; b < p.B; b += kThreads / 32) {
+    int* out = p.table_out + static_cast<size_t>(b) * p.width;
+    if (refused) {  // everything stays as it was
+      const int* in = p.table + static_cast<size_t>(b) * p.width;
+      for (int j = lane; j < p.width; j += 32) out[j] = in[j];
+      if (lane == 0) p.lens_out[b] = p.lens[b];
+      continue;
+    }
+    const int s = src[b], k = kept[b], want = ceil_pages(longer[b], p.page_log2), f = first[b];
+    const bool copy = s >= 0 && ceil_pages(len[s], p.page_log2) > k;
+    const int* in = p.table + static_cast<size_t>(max(s, 0)) * p.width;
+    for (int j = lane; j < p.width; j += 32) {
+      int page = -1;
+      if (j < k) {
+        page = in[j];
+        if (page < 0 || page >= p.P) paged::bad(paged::kBadPage);
+      } else if (j < want) {
+        page = list[f + j - k];
+        refs[page] = 1;
+        if (copy && j == k) {
+          const int of = in[j];
+          if (of >= 0 && of < p.P) {
+            const int c = atomicAdd(&s_copies, 1);
+            p.from[c] = of;
+            p.to[c] = page;
+          }
+        }
+      }
+      out[j] = page;
+    }
+    if (lane == 0) p.lens_out[b] = longer[b];
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int i = tid; i < p.P; i += kThreads) p.refs_out[i] = refused ? p.refs[i] : refs[i];
+  if (tid == 0) {
+    *p.n_copies = s_copies;
+    p.info[0] = max(need - n_free, 0);
+    p.info[1] = s_long;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) pages_compact_small_kernel(const Params p) {
+  extern __shared__ int sm[];
+  __shared__ int red[33];
+  int* refs = sm;          // [P]
+  int* hole = refs + p.P;  // free pages below n in order
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  paged::grid_wait();
+  paged::grid_launch_dependents();
+  int live = 0, n;
+#pragma unroll 4
+  for (int i = tid; i < p.P; i += kThreads) {
+    const int r = max(p.refs[i], 0);  // (negative counts are free pages, too)
+    refs[i] = r;
+    live += r > 0;
+  }
+  block_scan(live, red, &n);
+  __syncthreads();
+  const int moves = each_in_order(
+      n, red, [&](int i) { return refs[i] <= 0; },
+      [&](int i, int k) {
+        hole[k] = i;
+        p.to[k] = i;
+      });
+  __syncthreads();
+  // The k-th live page above n takes the k-th hole (there are as many of both).
+  each_in_order(
+      p.P - n, red, [&](int i) { return refs[n + i] > 0; },
+      [&](int i, int k) {
+        p.from[k] = n + i;
+        p.refs_out[hole[k]] = refs[n + i];
+        refs[n + i] = ~hole[k];  // negative: moved to hole[k]
+      });
+  __syncthreads();
+  for (int i = tid; i < p.P; i += kThreads) {
+    if (i >= n)
+      p.refs_out[i] = 0;
+    else if (refs[i] > 0)
+      p.refs_out[i] = refs[i];
+  }
+  for (int b = warp; b < p.B; b += kThreads / 32) {
+    const int l = p.lens[b], L = clamp_len(l, p), held = ceil_pages(L, p.page_log2);
+    if (lane == 0 && l > L) paged::bad(paged::kBadLength);
+    for (int j = lane; j < p.width; j += 32) {
+      const size_t e = static_cast<size_t>(b) * p.width + j;
+      int page = -1;
+      if (j < held) {
+        page = p.table[e];
+        if (page < 0 || page >= p.P || (page < n ? refs[page] <= 0 : refs[page] >= 0))
+          paged::bad(paged::kBadPage);  // (left as it was)
+        else if (page >= n)
+          page = ~refs[page];
+      }
+      p.table_out[e] = page;
+    }
+  }
+  if (tid == 0) {
+    *p.n_copies = moves;
+    p.info[0] = n;
+    p.info[1] = moves;
+  }
+}
+
 // Contents of the pages from[k] into to[k], k < *n_copies, in every layer of
 // both pools. A page of a pool is `page_bytes` in one piece (a multiple of 16).
 struct CopyParams {
@@ -354,6 +586,7 @@ struct CopyParams {
 
 __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CopyParams p) {
   paged::grid_wait();
+  paged::grid_launch_dependents();
   const int n = *p.n_copies;
   const int pieces = static_cast<int>((p.page_bytes + kCopyBytes - 1) / kCopyBytes);
   const long long units = static_cast<long long>(n) * p.layers * 2 * pieces;

@@ -166,6 +166,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long first = static_cast<long long>(blockIdx.x) * p.tokens_per_cta;
   const int count = static_cast<int>(min(static_cast<long long>(p.tokens_per_cta), p.tokens - first));
+  paged::grid_wait();  // (launched as a programmatic dependent: see launch_dependent)
+  paged::grid_launch_dependents();
   const int h0 = blockIdx.y * p.heads_per_cta;
   const int h1 = min(h0 + p.heads_per_cta, p.heads);
 
