@@ -487,22 +487,25 @@ inline int pages_setup(const attn_pages* c, int layers, long long layer_stride, 
   return ATTN_OK;
 }
 
-// One CTA settles the whole numbers when the counts fit its shared memory and
-// the tables have few entries, which it reads and writes alone.
+// One kernel does everything when the counts fit shared memory and the tables
+// have few entries (every CTA reads what its share of the rows needs, and the
+// rows that end or fork whole).
 #ifndef ETA_PAGES_SMALL_ENTRIES
 #define ETA_PAGES_SMALL_ENTRIES 65536
 #endif
 constexpr size_t kPagesSmallBytes = 200 * 1024;
 
-template <void (*kern)(pages::Params)>
-int pages_launch_small(const pages::Params& p, size_t words, cudaStream_t st) {
+template <void (*kern)(pages::Params, pages::CopyParams)>
+int pages_launch_small(const pages::Params& p, const pages::CopyParams& cp, size_t words, int ctas,
+                       cudaStream_t st) {
   static PerDeviceOnce attr;  // (one for each kernel)
   const cudaError_t e = attr.run([&]() {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(kPagesSmallBytes));
   });
   if (e != cudaSuccess) return cuda_fail(e);
-  return launch_dependent(kern, dim3(1), pages::kThreads, static_cast<int>(words * 4), st, p);
+  return launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), pages::kThreads,
+                          static_cast<int>(words * 4), st, p, cp);
 }
 
 template <bool UPDATE>
@@ -510,10 +513,18 @@ int pages_launch(pages::Params p, pages::CopyParams cp, cudaStream_t st) {
   DeviceInfo dev;
   if (device_info(&dev) != ATTN_OK) return ATTN_ERR_CUDA;
   if (!dev.sm100) return ATTN_ERR_UNSUPPORTED;
+  const size_t words = UPDATE ? pages::update_small_words(p.B, p.P) : pages::compact_small_words(p.P);
+  if (words * 4 <= kPagesSmallBytes &&
+      static_cast<long long>(p.B) * p.width <= ETA_PAGES_SMALL_ENTRIES) {
+    if constexpr (UPDATE)
+      return pages_launch_small<pages::pages_update_small_kernel>(p, cp, words, dev.sm_count, st);
+    else
+      return pages_launch_small<pages::pages_compact_small_kernel>(p, cp, words, dev.sm_count, st);
+  }
   size_t end = 0;
-  const auto part = [&end](size_t words) {
+  const auto part = [&end](size_t n) {
     const size_t at = end;
-    end = align_up(end + words * 4, 256);
+    end = align_up(end + n * 4, 256);
     return at;
   };
   const size_t B = static_cast<size_t>(p.B), P = static_cast<size_t>(p.P);
@@ -534,17 +545,8 @@ int pages_launch(pages::Params p, pages::CopyParams cp, cudaStream_t st) {
   cp.from = p.from;
   cp.to = p.to;
   cp.n_copies = p.n_copies;
-  const size_t words = UPDATE ? pages::update_small_words(p.B, p.P) : pages::compact_small_words(p.P);
-  const bool small = words * 4 <= kPagesSmallBytes &&
-                     static_cast<long long>(p.B) * p.width <= ETA_PAGES_SMALL_ENTRIES;
-  if constexpr (UPDATE)
-    rc = small ? pages_launch_small<pages::pages_update_small_kernel>(p, words, st)
-               : launch_dependent(pages::pages_update_kernel, dim3(pages::kCtas), pages::kThreads, 0,
-                                  st, p);
-  else
-    rc = small ? pages_launch_small<pages::pages_compact_small_kernel>(p, words, st)
-               : launch_dependent(pages::pages_compact_kernel, dim3(pages::kCtas), pages::kThreads, 0,
-                                  st, p);
+  rc = launch_dependent(UPDATE ? pages::pages_update_kernel : pages::pages_compact_kernel,
+                        dim3(pages::kCtas), pages::kThreads, 0, st, p);
   if (rc == ATTN_OK)
     rc = launch_dependent(pages::pages_copy_kernel, dim3(static_cast<unsigned>(6 * dev.sm_count)),
                           pages::kCopyThreads, 0, st, cp);
@@ -557,7 +559,7 @@ int pages_update(const attn_pages* c, int layers, long long layer_stride, const 
                  cudaStream_t st) {
   paged::Cache cache;
   pages::Params p = {};
-  pages::CopyParams cp;
+  pages::CopyParams cp = {};
   const int rc = pages_setup(c, layers, layer_stride, B, lens, refs, table_out, refs_out, info,
                              &cache, &p, &cp);
   if (rc != ATTN_OK) return rc;
@@ -575,7 +577,7 @@ int pages_compact(const attn_pages* c, int layers, long long layer_stride, const
                   cudaStream_t st) {
   paged::Cache cache;
   pages::Params p = {};
-  pages::CopyParams cp;
+  pages::CopyParams cp = {};
   const int rc = pages_setup(c, layers, layer_stride, B, lens, refs, table_out, refs_out, info,
                              &cache, &p, &cp);
   if (rc != ATTN_OK) return rc;

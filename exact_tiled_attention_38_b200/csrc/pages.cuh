@@ -1,10 +1,11 @@
 // Page operations of a paged cache: rows taking over other rows (forks, beam
 // steps, ended and new sequences) and growing, and compaction of the live
 // pages. Both first settle the whole numbers (block tables, reference counts,
-// which page goes where), then copy page contents with the whole grid. The
-// whole numbers are one CTA's work when the counts fit its shared memory and
-// the tables are not large, else a cluster's, whose hardware barrier stands
-// between the steps.
+// which page goes where), then copy page contents with the whole grid. When the
+// counts fit shared memory and the tables are not large, one kernel does both:
+// every CTA settles all of the whole numbers for itself, and writes and copies
+// its share. Otherwise a cluster of CTAs settles them, its hardware barrier
+// between the steps, and a second kernel copies.
 //
 // Free pages are those with a reference count <= 0, and are always taken
 // lowest first in the order of the rows, so the result does not depend on
@@ -35,7 +36,7 @@ constexpr int kCtas = 8;
 constexpr int kThreads = 1024;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 4;
-constexpr int kCopyBytes = kCopyThreads * 16 * kCopyUnroll;  // one CTA's piece of a copy
+constexpr int kCopyBytes = 32 * 16 * kCopyUnroll;  // one warp's piece of a copy
 
 __device__ __forceinline__ int cta_rank() {
   uint32_t r;
@@ -56,6 +57,59 @@ __device__ __forceinline__ void cluster_barrier() {
 // launch go past L1.
 __device__ __forceinline__ int ld(const int* p) { return __ldcg(p); }
 __device__ __forceinline__ void st(int* p, int v) { __stcg(p, v); }
+
+// The pools whose pages are copied. A page of a pool is `page_bytes` in one
+// piece (a multiple of 16), in every layer of both pools.
+struct CopyParams {
+  uint8_t* pool[2];
+  long long page_stride;   // bytes
+  long long layer_stride;  // bytes
+  long long page_bytes;
+  int layers;
+  const int* from;
+  const int* to;
+  const int* n_copies;
+};
+
+// Contents of the pages from[k] into to[k], k < n: pieces of 2 KB, one a warp
+// at a time, `warps` warps in all.
+__device__ __forceinline__ void copy_pages(const CopyParams& p, const int* from, const int* to,
+                                           int n, long long me, long long warps) {
+  const int lane = threadIdx.x & 31;
+  const unsigned pieces = static_cast<unsigned>((p.page_bytes + kCopyBytes - 1) / kCopyBytes);
+  const unsigned per_page = pieces * 2u * static_cast<unsigned>(p.layers);
+  const long long units = static_cast<long long>(n) * per_page;
+  for (long long w = me; w < units; w += warps) {
+    unsigned k, r;
+    if (units <= 0xffffffffLL) {
+      k = static_cast<unsigned>(w) / per_page;
+      r = static_cast<unsigned>(w) - k * per_page;
+    } else {
+      k = static_cast<unsigned>(w / per_page);
+      r = static_cast<unsigned>(w - static_cast<long long>(k) * per_page);
+    }
+    const unsigned half = r / pieces, piece = r - half * pieces;  // (layer, pool)
+    uint8_t* base = ((half & 1) ? p.pool[1] : p.pool[0]) + (half >> 1) * p.layer_stride;
+    const long long at = static_cast<long long>(piece) * kCopyBytes + lane * 16;
+    const uint8_t* src = base + from[k] * p.page_stride + at;
+    uint8_t* dst = base + to[k] * p.page_stride + at;
+    uint4 v[kCopyUnroll];
+#pragma unroll
+    for (int i = 0; i < kCopyUnroll; ++i)
+      if (at + i * 512 < p.page_bytes) v[i] = *reinterpret_cast<const uint4*>(src + i * 512);
+#pragma unroll
+    for (int i = 0; i < kCopyUnroll; ++i)
+      if (at + i * 512 < p.page_bytes) *reinterpret_cast<uint4*>(dst + i * 512) = v[i];
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CopyParams p) {
+  paged::grid_wait();
+  paged::grid_launch_dependents();
+  constexpr int W = kCopyThreads / 32;
+  copy_pages(p, p.from, p.to, *p.n_copies, static_cast<long long>(blockIdx.x) * W + threadIdx.x / 32,
+             static_cast<long long>(gridDim.x) * W);
+}
 
 // Exclusive prefix of v over the block's threads; *total gets the sum. `red`
 // holds 33 words.
@@ -342,11 +396,13 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-// ------------------------------------------------------------------ one CTA
-// The same two operations by one CTA with the counts in its shared memory.
+// ------------------------------------------------------------------ one kernel
+// The same two operations with the counts in every CTA's shared memory.
 
 // Words of dynamic shared memory.
-inline size_t update_small_words(int B, int P) { return 2 * static_cast<size_t>(P) + 7 * static_cast<size_t>(B) + 1; }
+inline size_t update_small_words(int B, int P) {
+  return 2 * static_cast<size_t>(P) + 9 * static_cast<size_t>(B) + 1;
+}
 inline size_t compact_small_words(int P) { return 2 * static_cast<size_t>(P); }
 
 // Calls f(i, rank) for the entries i of [0, n) where pick(i) holds, rank being
@@ -381,13 +437,14 @@ __device__ __forceinline__ int each_in_order(int n, int* red, Pick pick, F f) {
   return all;
 }
 
-// A row of s tokens' worth that k rows go on from: its full pages' counts
-// change by k - 1, its last, partly filled page's by -1 if k = 0. Rows that
-// just go on (k = 1) need not be read for that.
-__global__ void __launch_bounds__(kThreads, 1) pages_update_small_kernel(const Params p) {
+// Of a row that k rows go on from, the counts of the full pages change by k - 1,
+// that of the last, partly filled page by -1 if k = 0. Rows that just go on
+// (k = 1) need not be read for that.
+__global__ void __launch_bounds__(kThreads, 1)
+    pages_update_small_kernel(const Params p, const CopyParams cp) {
   extern __shared__ int sm[];
   __shared__ int red[33];
-  __shared__ int s_copies, s_long;
+  __shared__ int s_long;
   int* refs = sm;               // [P]
   int* list = refs + p.P;       // [P] free pages in order
   int* len = list + p.P;        // [B]
@@ -396,8 +453,11 @@ __global__ void __launch_bounds__(kThreads, 1) pages_update_small_kernel(const P
   int* keeper = longer + p.B;   // [B]
   int* takers = keeper + p.B;   // [B]
   int* kept = takers + p.B;     // [B]
-  int* first = kept + p.B;      // [B + 1] fresh pages before each row
+  int* from = kept + p.B;       // [B] copies
+  int* to = from + p.B;         // [B]
+  int* first = to + p.B;        // [B + 1] fresh pages before each row
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int me = blockIdx.x * (kThreads / 32) + warp, warps = gridDim.x * (kThreads / 32);
   paged::grid_wait();
   paged::grid_launch_dependents();
 
@@ -413,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_update_small_kernel(const P
   }
 #pragma unroll 4
   for (int i = tid; i < p.P; i += kThreads) refs[i] = p.refs[i];
-  if (tid == 0) s_copies = s_long = 0;
+  if (tid == 0) s_long = 0;
   __syncthreads();
 
   for (int b = tid; b < p.B; b += kThreads) {
@@ -467,7 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1) pages_update_small_kernel(const P
   const bool refused = need > n_free || s_long > 0;
   __syncthreads();
 
-  for (int b = warp; b < p.B; b += kThreads / 32) {
+  // The tables, a share of the rows.
+  for (int b = me; b < p.B; b += warps) {
     int* out = p.table_out + static_cast<size_t>(b) * p.width;
     if (refused) {  // everything stays as it was
       const int* in = p.table + static_cast<size_t>(b) * p.width;
@@ -475,9 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1) pages_update_small_kernel(const P
       if (lane == 0) p.lens_out[b] = p.lens[b];
       continue;
     }
-    const int s = src[b], k = kept[b], want = ceil_pages(longer[b], p.page_log2), f = first[b];
-    const bool copy = s >= 0 && ceil_pages(len[s], p.page_log2) > k;
-    const int* in = p.table + static_cast<size_t>(max(s, 0)) * p.width;
+    const int k = kept[b], want = ceil_pages(longer[b], p.page_log2), f = first[b];
+    const int* in = p.table + static_cast<size_t>(max(src[b], 0)) * p.width;
     for (int j = lane; j < p.width; j += 32) {
       int page = -1;
       if (j < k) {
@@ -485,36 +545,46 @@ __global__ void __launch_bounds__(kThreads, 1) pages_update_small_kernel(const P
         if (page < 0 || page >= p.P) paged::bad(paged::kBadPage);
       } else if (j < want) {
         page = list[f + j - k];
-        refs[page] = 1;
-        if (copy && j == k) {
-          const int of = in[j];
-          if (of >= 0 && of < p.P) {
-            const int c = atomicAdd(&s_copies, 1);
-            p.from[c] = of;
-            p.to[c] = page;
-          }
-        }
       }
       out[j] = page;
     }
     if (lane == 0) p.lens_out[b] = longer[b];
   }
-  __syncthreads();
-#pragma unroll 4
-  for (int i = tid; i < p.P; i += kThreads) p.refs_out[i] = refused ? p.refs[i] : refs[i];
-  if (tid == 0) {
-    *p.n_copies = s_copies;
+  if (refused) {
+    for (int i = blockIdx.x * kThreads + tid; i < p.P; i += gridDim.x * kThreads)
+      p.refs_out[i] = p.refs[i];
+  } else {
+    for (int k = tid; k < need; k += kThreads) refs[list[k]] = 1;
+  }
+  if (blockIdx.x == 0 && tid == 0) {
     p.info[0] = max(need - n_free, 0);
     p.info[1] = s_long;
   }
+  if (refused) return;
+  // The copies, in the order of the rows.
+  const int copies = each_in_order(
+      p.B, red,
+      [&](int b) { return src[b] >= 0 && ceil_pages(len[src[b]], p.page_log2) > kept[b]; },
+      [&](int b, int k) {
+        const int of = p.table[static_cast<size_t>(src[b]) * p.width + kept[b]], page = list[first[b]];
+        from[k] = of >= 0 && of < p.P ? of : page;  // (a bad id was reported: nothing to copy)
+        to[k] = page;
+      });
+  __syncthreads();
+  for (int i = blockIdx.x * kThreads + tid; i < p.P; i += gridDim.x * kThreads)
+    p.refs_out[i] = refs[i];
+  copy_pages(cp, from, to, copies, me, warps);
 }
 
-__global__ void __launch_bounds__(kThreads, 1) pages_compact_small_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    pages_compact_small_kernel(const Params p, const CopyParams cp) {
   extern __shared__ int sm[];
   __shared__ int red[33];
-  int* refs = sm;          // [P]
-  int* hole = refs + p.P;  // free pages below n in order
+  int* refs = sm;              // [P]
+  int* to = refs + p.P;        // [P / 2] free pages below n in order
+  int* from = to + p.P / 2;    // [P / 2] live pages from n on in order
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int me = blockIdx.x * (kThreads / 32) + warp, warps = gridDim.x * (kThreads / 32);
   paged::grid_wait();
   paged::grid_launch_dependents();
   int live = 0, n;
@@ -526,29 +596,22 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_small_kernel(const 
   }
   block_scan(live, red, &n);
   __syncthreads();
+  // The k-th live page from n on takes the k-th hole below n; there are as many
+  // of both, so not more than P / 2.
   const int moves = each_in_order(
-      n, red, [&](int i) { return refs[i] <= 0; },
-      [&](int i, int k) {
-        hole[k] = i;
-        p.to[k] = i;
-      });
+      n, red, [&](int i) { return refs[i] <= 0; }, [&](int i, int k) { to[k] = i; });
   __syncthreads();
-  // The k-th live page above n takes the k-th hole (there are as many of both).
   each_in_order(
       p.P - n, red, [&](int i) { return refs[n + i] > 0; },
       [&](int i, int k) {
-        p.from[k] = n + i;
-        p.refs_out[hole[k]] = refs[n + i];
-        refs[n + i] = ~hole[k];  // negative: moved to hole[k]
+        from[k] = n + i;
+        refs[to[k]] = refs[n + i];
+        refs[n + i] = ~to[k];  // negative: it moves to to[k]
       });
   __syncthreads();
-  for (int i = tid; i < p.P; i += kThreads) {
-    if (i >= n)
-      p.refs_out[i] = 0;
-    else if (refs[i] > 0)
-      p.refs_out[i] = refs[i];
-  }
-  for (int b = warp; b < p.B; b += kThreads / 32) {
+  for (int i = blockIdx.x * kThreads + tid; i < p.P; i += gridDim.x * kThreads)
+    p.refs_out[i] = i < n ? refs[i] : 0;
+  for (int b = me; b < p.B; b += warps) {
     const int l = p.lens[b], L = clamp_len(l, p), held = ceil_pages(L, p.page_log2);
     if (lane == 0 && l > L) paged::bad(paged::kBadLength);
     for (int j = lane; j < p.width; j += 32) {
@@ -556,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_small_kernel(const 
       int page = -1;
       if (j < held) {
         page = p.table[e];
-        if (page < 0 || page >= p.P || (page < n ? refs[page] <= 0 : refs[page] >= 0))
+        if (page < 0 || page >= p.P || p.refs[page] <= 0)
           paged::bad(paged::kBadPage);  // (left as it was)
         else if (page >= n)
           page = ~refs[page];
@@ -564,51 +627,11 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_small_kernel(const 
       p.table_out[e] = page;
     }
   }
-  if (tid == 0) {
-    *p.n_copies = moves;
+  if (blockIdx.x == 0 && tid == 0) {
     p.info[0] = n;
     p.info[1] = moves;
   }
-}
-
-// Contents of the pages from[k] into to[k], k < *n_copies, in every layer of
-// both pools. A page of a pool is `page_bytes` in one piece (a multiple of 16).
-struct CopyParams {
-  uint8_t* pool[2];
-  long long page_stride;   // bytes
-  long long layer_stride;  // bytes
-  long long page_bytes;
-  int layers;
-  const int* from;
-  const int* to;
-  const int* n_copies;
-};
-
-__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CopyParams p) {
-  paged::grid_wait();
-  paged::grid_launch_dependents();
-  const int n = *p.n_copies;
-  const int pieces = static_cast<int>((p.page_bytes + kCopyBytes - 1) / kCopyBytes);
-  const long long units = static_cast<long long>(n) * p.layers * 2 * pieces;
-  for (long long w = blockIdx.x; w < units; w += gridDim.x) {
-    const int piece = static_cast<int>(w % pieces);
-    const long long r = w / pieces;
-    const int layer = static_cast<int>((r >> 1) % p.layers);
-    const int k = static_cast<int>((r >> 1) / p.layers);
-    uint8_t* base = p.pool[r & 1] + layer * p.layer_stride;
-    const uint8_t* src = base + p.from[k] * p.page_stride;
-    uint8_t* dst = base + p.to[k] * p.page_stride;
-    const long long at = static_cast<long long>(piece) * kCopyBytes + threadIdx.x * 16;
-    uint4 v[kCopyUnroll];
-#pragma unroll
-    for (int i = 0; i < kCopyUnroll; ++i)
-      if (at + i * kCopyThreads * 16 < p.page_bytes)
-        v[i] = *reinterpret_cast<const uint4*>(src + at + i * kCopyThreads * 16);
-#pragma unroll
-    for (int i = 0; i < kCopyUnroll; ++i)
-      if (at + i * kCopyThreads * 16 < p.page_bytes)
-        *reinterpret_cast<uint4*>(dst + at + i * kCopyThreads * 16) = v[i];
-  }
+  copy_pages(cp, from, to, moves, me, warps);
 }
 
 }  // namespace pages
