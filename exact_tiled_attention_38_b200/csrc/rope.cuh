@@ -14,9 +14,13 @@
 // rounds once, to the type of the output.
 //
 // Bound by memory: every value is read once and written once. A CTA takes a
-// few tokens and some of their heads: first the tokens' cosines and sines go
-// to shared memory, then each thread keeps the eight pairs of its place in the
-// row in registers and goes through the heads with 16-byte loads.
+// few tokens and some of their heads: the first heads' values are loaded, the
+// tokens' cosines and sines go to shared memory, then each thread keeps the
+// eight pairs of its place in the row in registers and goes through the heads
+// with 16-byte loads. Measured on B200, of the 6554 GB/s of a copy: q and k of
+// 4 x 16 + 16 heads x 2048 x 128 24.9 us (0.82; all launches of this length
+// lose about 4 us at both ends), 32 + 8 heads x 32768 x 64 55.7 us (0.92), an
+// append of 9 chunks of up to 1801 tokens 51.7 us (0.85).
 #pragma once
 
 #include "paged_common.cuh"
@@ -28,7 +32,7 @@ constexpr int kThreads = 256;
 constexpr int kSlots = 64;                    // (token, unit) places of a CTA
 constexpr int kGroups = kThreads / kSlots;    // threads that share a place, by heads
 constexpr int kMaxTokens = 32;                // tokens of a CTA
-constexpr int kHeadsAtOnce = 4;               // heads a thread loads before it stores any
+constexpr int kHeadsAtOnce = 2;               // heads a thread loads before it stores any
 
 struct Tensor {
   const void* x;
@@ -171,6 +175,27 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
   const int h0 = blockIdx.y * p.heads_per_cta;
   const int h1 = min(h0 + p.heads_per_cta, p.heads);
 
+  // This thread's place in a row: token t, the two 8-value pieces at c0 and c1.
+  const int slot = tid % kSlots;
+  const int t_mine = VEC ? slot / p.units : 0, u_mine = slot - t_mine * p.units;
+  const int nrot = p.rot >> 4;
+  const bool turned = u_mine < nrot;
+  const int c0 = !turned ? p.rot + (u_mine - nrot) * 16 : INTERLEAVED ? u_mine * 16 : u_mine * 8;
+  const int c1 = turned && !INTERLEAVED ? c0 + half : c0 + 8;
+  const bool mine = VEC && t_mine < count, second = c1 < p.d;
+  uint4 a[kHeadsAtOnce], b[kHeadsAtOnce];
+  auto load = [&](int h) {  // the pieces of heads h, h + kGroups, ...
+#pragma unroll
+    for (int i = 0; i < kHeadsAtOnce; ++i) {
+      if (h + i * kGroups >= h1) break;
+      const Row<T> r = row_of<T, APPEND>(p, first + t_mine, h + i * kGroups, 0);
+      a[i] = *reinterpret_cast<const uint4*>(r.x + c0);
+      if (second) b[i] = *reinterpret_cast<const uint4*>(r.x + c1);
+    }
+  };
+  // The first heads' values are on their way while the angles are worked out.
+  if (mine) load(h0 + tid / kSlots);
+
   if constexpr (APPEND) {
     // One warp per token: its sequence, its position, its page.
     for (int t = warp; t < count; t += kThreads / 32) {
@@ -230,45 +255,22 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
   __syncthreads();
 
   if constexpr (VEC) {
-    const int slot = tid % kSlots;
-    const int t = slot / p.units, u = slot - t * p.units;
-    if (t >= count) return;
-    const long long token = first + t;
-    const long long page = APPEND ? place[t].page : 0;
-    const int nrot = p.rot >> 4;
-    const bool turned = u < nrot;
-    // The two 8-value pieces of this place.
-    int c0, c1;
-    if (turned) {
-      c0 = INTERLEAVED ? u * 16 : u * 8;
-      c1 = INTERLEAVED ? c0 + 8 : c0 + half;
-    } else {
-      c0 = p.rot + (u - nrot) * 16;
-      c1 = c0 + 8;
-    }
-    const bool second = c1 < p.d;
+    if (!mine) return;
+    const long long page = APPEND ? place[t_mine].page : 0;
     float co[8], si[8];
     if (turned) {
       const float4* t4 = reinterpret_cast<const float4*>(table);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4 w = t4[(t * 4 + j) * nrot + u];
+        const float4 w = t4[(t_mine * 4 + j) * nrot + u_mine];
         co[2 * j] = w.x, si[2 * j] = w.y, co[2 * j + 1] = w.z, si[2 * j + 1] = w.w;
       }
     }
-    for (int h = h0 + tid / kSlots; h < h1; h += kGroups * kHeadsAtOnce) {
-      uint4 a[kHeadsAtOnce], b[kHeadsAtOnce];
+    for (int h = h0 + tid / kSlots; h < h1;) {
 #pragma unroll
       for (int i = 0; i < kHeadsAtOnce; ++i) {
         if (h + i * kGroups >= h1) break;
-        const Row<T> r = row_of<T, APPEND>(p, token, h + i * kGroups, page);
-        a[i] = *reinterpret_cast<const uint4*>(r.x + c0);
-        if (second) b[i] = *reinterpret_cast<const uint4*>(r.x + c1);
-      }
-#pragma unroll
-      for (int i = 0; i < kHeadsAtOnce; ++i) {
-        if (h + i * kGroups >= h1) break;
-        const Row<T> r = row_of<T, APPEND>(p, token, h + i * kGroups, page);
+        const Row<T> r = row_of<T, APPEND>(p, first + t_mine, h + i * kGroups, page);
         if (r.y == nullptr) continue;
         if (turned && r.turn) {
           float x[8], y[8];
@@ -296,6 +298,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
         *reinterpret_cast<uint4*>(r.y + c0) = a[i];
         if (second) *reinterpret_cast<uint4*>(r.y + c1) = b[i];
       }
+      h += kGroups * kHeadsAtOnce;
+      if (h < h1) load(h);
     }
   } else {
     // Pair by pair, then value by value: any even rot.
