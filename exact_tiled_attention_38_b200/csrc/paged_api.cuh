@@ -257,9 +257,9 @@ int paged_run(const void* q, long long q_stride, const attn_pages* pages, const 
   const int tt = paged::BM / G;
   // (a CTA's steps are counted in 32 bits: with the longest cache that the
   // table allows for every token, this is years of work)
-  if ((static_cast<double>(total_q) / (paged::NQT * tt) + B) * c.Hkv *
-          (static_cast<double>(c.capacity()) / paged::BN + 1) / info.sm_count > 2e9)
-    return ATTN_ERR_UNSUPPORTED;
+  const double most_steps = (static_cast<double>(total_q) / (paged::NQT * tt) + B) * c.Hkv *
+                            (static_cast<double>(c.capacity()) / paged::BN + 1);
+  if (most_steps / info.sm_count > 2e9) return ATTN_ERR_UNSUPPORTED;
   CUtensorMap tq, tk, tv;
   int rc = encode_queries(&tq, q, q_stride, c, G, total_q, tt, bf16);
   if (rc == ATTN_OK) rc = encode_pools(&tk, &tv, c, bf16);
@@ -285,6 +285,7 @@ int paged_run(const void* q, long long q_stride, const attn_pages* pages, const 
   p.window = window;
   p.nc = info.sm_count;
   p.inline_plan = B <= paged::kInlineB ? 1 : 0;
+  p.warp_plan = B <= 32 && most_steps < 1e9 ? 1 : 0;
   p.max_pairs = (max_q + paged::NQT * tt - 1) / (paged::NQT * tt);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_ns = kDefaultWaitNs;

@@ -106,7 +106,8 @@ struct Cfg {
   // o_done[2], s_free[2], pv_done[2], x_up, x_down, drain
   static constexpr int kNumBars = 2 * kStages + 7 * NQT + 3;
   static constexpr int kCtlOff = kBarOff + kNumBars * 8;
-  // (m, l) of group 1's rows, where its output would be staged (it stages none then).
+  // A warp of group 1 hands its rows' (m, l) over where it stages output at other
+  // times. (Its own place: its neighbours may still be storing the last piece's.)
   static constexpr int kXOff = kStgOff + 4 * kStgWarpBytes;
   static constexpr int kWalkOff = kCtlOff + 64;  // each warp's way through the range
   static constexpr int kSmemBytes = kWalkOff + 10 * 96 + 1024;  // + runtime 1024-byte alignment
@@ -163,6 +164,7 @@ struct Params {
   int window;
   int nc;
   int inline_plan;  // no plan kernel
+  int warp_plan;    // up to 32 sequences, steps in 32 bits: a warp can make the plan
   int max_pairs;    // tile pairs that a sequence of max_q tokens has
   long long l2_bytes;
   float scale_log2;
@@ -398,6 +400,83 @@ __device__ __forceinline__ Start plan_find(const Params& p, const Head& h, const
   return st;
 }
 
+// The same for up to 32 sequences whose steps count in 32 bits and go in
+// contiguous ranges, by one warp for itself: a lane per sequence, no barriers,
+// little code (a kernel's start runs on cold instruction and data caches: with
+// the block's plan a stream began its loads 10,000 cycles after its start, with
+// this one 5,000). False: the block has to make the plan.
+__device__ __forceinline__ bool plan_warp(const Params& p, int c, int lane, Head& h, Start& st) {
+  Seq s{0, 0, 0};
+  if (lane < p.B) s = load_seq(p.cu_q, p.lens, lane, p.total_q, p.max_q, p.capacity());
+  const int n = pairs_of(p, s.T);
+  int mine = 0;
+  float keys = s.T > 0 ? static_cast<float>(s.L) : 0.f;
+  if (p.max_pairs <= 32) {
+    for (int i = 0; i < n; ++i) mine += span_of(p, s, i).n;
+  } else {
+    for (int b = 0; b < p.B; ++b) {  // long chunks: the lanes share a sequence's pairs
+      const Seq t{0, __shfl_sync(0xffffffffu, s.T, b), __shfl_sync(0xffffffffu, s.L, b)};
+      const int m = pairs_of(p, t.T);
+      int sum = 0;
+      for (int i = lane; i < m; i += 32) sum += span_of(p, t, i).n;
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      if (lane == b) mine = sum;
+    }
+  }
+  mine *= p.Hkv;
+  int x = mine;  // inclusive prefix
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    keys += __shfl_xor_sync(0xffffffffu, keys, o);
+    if (lane >= o) x += y;
+  }
+  if (keys * p.Hkv * p.d * 4.f > static_cast<float>(p.l2_bytes / 2)) return false;
+  const unsigned steps = __shfl_sync(0xffffffffu, x, 31);
+  const unsigned want = (steps + kMinSteps - 1) / kMinSteps;
+  const unsigned busy = min(want, static_cast<unsigned>(p.nc));
+  const unsigned w = busy > 0 ? (steps + busy - 1) / busy : 1;
+  h.steps = h.rest = steps;
+  h.w = w;
+  h.chunks = 0;
+  h.ctas = static_cast<int>((steps + w - 1) / w);
+  if (c >= h.ctas) return true;
+  const int at = c * static_cast<int>(w);
+  const int b = __ffs(__ballot_sync(0xffffffffu, x > at)) - 1;
+  const Seq t{0, __shfl_sync(0xffffffffu, s.T, b), __shfl_sync(0xffffffffu, s.L, b)};
+  const unsigned per_head = static_cast<unsigned>(__shfl_sync(0xffffffffu, mine, b)) / p.Hkv;
+  unsigned r = at - __shfl_sync(0xffffffffu, x - mine, b);
+  st.b = b;
+  st.g = static_cast<int>(r / per_head);
+  r -= st.g * per_head;
+  st.rest = at - static_cast<int>(r);
+  st.chunk = 0;
+  st.pad = 0;
+  st.pair = st.i = 0;
+  const int m = pairs_of(p, t.T);
+  for (int i0 = 0; i0 < m; i0 += 32) {
+    const int k = i0 + lane < m ? span_of(p, t, i0 + lane).n : 0;
+    int y = k;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    const unsigned over = __ballot_sync(0xffffffffu, static_cast<int>(r) < y);
+    if (over != 0) {
+      const int l = __ffs(over) - 1, before = __shfl_sync(0xffffffffu, y - k, l);
+      st.pair = i0 + l;
+      st.i = static_cast<int>(r) - before;
+      st.rest += before;
+      break;
+    }
+    const int all = __shfl_sync(0xffffffffu, y, 31);
+    r -= all;
+    st.rest += all;
+  }
+  return true;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) attn_paged_plan_kernel(const Params p) {
   __shared__ long long red[2 * kPlanThreads / 32];
   grid_launch_dependents();
@@ -523,7 +602,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = x_down + 1;
   CtaCtl* ctl = reinterpret_cast<CtaCtl*>(smem + C::kCtlOff);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kCtlOff + 32);
-  float2* xrow = reinterpret_cast<float2*>(smem + C::kXOff);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -568,21 +646,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_launch_dependents();
   Walk& w = *reinterpret_cast<Walk*>(smem + C::kWalkOff + warp * 96);
   bool work;
-  if (p.inline_plan) {
+  Head h;
+  Start st;
+  if (p.warp_plan && plan_warp(p, c, lane, h, st)) {  // (the same answer in every warp)
+    work = c < h.ctas;
+    if (work) {
+      if (lane == 0) w.start(p, h, st, c);
+      __syncwarp();
+      if (threadIdx.x == 0) p.plan.starts[c] = st;  // for the gather, as is the head
+    }
+    if (c == 0 && warp == 0) {
+      if (lane == 0) *p.plan.head = h;
+      if (lane < p.B) check_seq(p.cu_q, p.lens, lane, p.total_q, p.max_q, p.capacity());
+    }
+  } else if (p.inline_plan) {
     long long* rest_at = reinterpret_cast<long long*>(smem + C::kStgOff);
     int* chunk_at = reinterpret_cast<int*>(rest_at + p.B + 1);
-    const Head h = make_plan<kThreads>(p, rest_at, chunk_at,
+    h = make_plan<kThreads>(p, rest_at, chunk_at,
                                        reinterpret_cast<long long*>(smem + C::kWalkOff), c == 0);
     work = c < h.ctas;
     if (work) {
-      const Start st = plan_find(p, h, rest_at, chunk_at, c, lane);  // (every warp for itself)
+      st = plan_find(p, h, rest_at, chunk_at, c, lane);  // (every warp for itself)
       if (lane == 0) w.start(p, h, st, c);
       if (threadIdx.x == 0) p.plan.starts[c] = st;  // for the gather, as is the head
     }
     if (c == 0 && threadIdx.x == 0) *p.plan.head = h;
     __syncthreads();  // the scratch is free for the softmax warps
   } else {
-    const Head h = *p.plan.head;
+    h = *p.plan.head;
     work = c < h.ctas;
     if (work && lane == 0) w.start(p, h, p.plan.starts[c], c);
     __syncwarp();
@@ -954,10 +1045,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool two = w.two(p);
       const bool shared = !two && w.steps() > 1;  // group 1 has a part of the same rows
       const int r = (warp & 3) * 32 + lane;       // row of the tile
+      float2* xrow =
+          reinterpret_cast<float2*>(smem + C::kXOff + (warp & 3) * C::kStgWarpBytes) + lane;
       if (!two && t == 1) {
         if (shared) {
           // Hand (m, l) to group 0 and wait until it has read O_1.
-          xrow[r] = make_float2(m, l);
+          *xrow = make_float2(m, l);
           mbar_arrive(x_up);
           ok = warp_all(wait_bar(x_down, w.xp & 1, ctl, kSiteXDown));
           __syncwarp();
@@ -974,7 +1067,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (shared) {
         if (!(ok = warp_all(wait_bar(&o_done[1], w.od1 & 1, ctl, kSiteODone)))) break;
         if (!(ok = warp_all(wait_bar(x_up, w.xp & 1, ctl, kSiteXUp)))) break;
-        const float2 other = xrow[r];
+        const float2 other = *xrow;
         const float mm = fmaxf(m, other.x);
         w0 = m == -INFINITY ? 0.f : ex2_approx(m - mm);
         w1 = other.x == -INFINITY ? 0.f : ex2_approx(other.x - mm);
@@ -1095,12 +1188,13 @@ __global__ void __launch_bounds__(256) attn_paged_gather_kernel(const Params p) 
   constexpr int CW = D / 32;  // 4-column units of a thread
   __shared__ __align__(16) uint8_t stage[32 * (2 * D + 16)];
   grid_wait();
-  const Head h = *p.plan.head;
   const int c = blockIdx.x;
+  const Head h = *p.plan.head;  // (loaded together; a start that no CTA wrote is not looked at)
+  const Start at_c = p.plan.starts[c], at_next = p.plan.starts[min(c + 1, p.nc - 1)];
   if (c >= h.ctas) return;
   const bool has_chunks = c < h.chunks;
   if (!has_chunks && c + 1 >= h.ctas) return;
-  const Start nx = p.plan.starts[has_chunks ? c : c + 1];
+  const Start nx = has_chunks ? at_c : at_next;
   const Seq s = load_seq(p.cu_q, p.lens, nx.b, p.total_q, p.max_q, p.capacity());
   const int tile = blockIdx.y / 4, t0 = (nx.pair * NQT + tile) * p.tt;
   const int r0 = (blockIdx.y & 3) * 32;  // rows r0 .. r0 + 31 of the tile

@@ -238,6 +238,124 @@ def test_agrees_with_contiguous_prefill_and_packed_decode(lib):
     assert (l1 - ld).abs().max() < 1e-4
 
 
+def plain(q, kp, vp, table, T, L, scale, window, rows):
+    """(which, o, lse, sum p |v|, sum of the visible |v|) in 64 bits on the GPU, of up to `rows` new
+    tokens of each sequence (the first, the last, some between)."""
+    Hq, d = q.shape[1:]
+    Hkv, page = kp.shape[1], kp.shape[2]
+    at, picked, out, ls, pv, av = 0, [], [], [], [], []
+    for b, (t, l) in enumerate(zip(T, L)):
+        if t:
+            i = torch.linspace(0, t - 1, min(t, rows)).long().unique().cuda()
+            ids = table[b, :-(-l // page)].long()
+            j, pos = torch.arange(l, device="cuda"), l - t + i
+            see = j[None] <= pos[:, None]
+            if window:
+                see &= j[None] > pos[:, None] - window
+            ob = torch.zeros(len(i), Hq, d, dtype=torch.float64, device="cuda")
+            wb, ab = torch.zeros_like(ob), torch.zeros_like(ob)
+            lb = torch.full((len(i), Hq), -torch.inf, dtype=torch.float64, device="cuda")
+            for h in range(Hq if l else 0):
+                k = kp[ids, h // (Hq // Hkv)].reshape(-1, d)[:l].double()
+                v = vp[ids, h // (Hq // Hkv)].reshape(-1, d)[:l].double()
+                s = torch.where(see, q[at + i, h].double() @ k.T * scale, -torch.inf)
+                lb[:, h] = torch.logsumexp(s, -1)
+                some = torch.isfinite(lb[:, h])
+                p = torch.exp(s[some] - lb[some, h, None])
+                ob[some, h] = p @ v
+                wb[some, h] = p @ v.abs()
+                ab[some, h] = see[some].double() @ v.abs()
+            pv.append(wb)
+            av.append(ab)
+            picked.append(at + i)
+            out.append(ob)
+            ls.append(lb)
+        at += t
+    return [torch.cat(x) for x in (picked, out, ls, pv, av)]
+
+
+# The shapes on which the steps are dealt out in other ways: caches beyond L2 (chunks of items
+# in step, rests to the other CTAs, whole items that begin anywhere), batches that a block or a
+# kernel of its own plans, chunks of many tile pairs.
+BIG = {
+    "chunks_beyond_l2": ("bf16", 128, 8, 8, 64, [300], [20011], 0),
+    "chunks_beyond_l2_group_4": ("bf16", 128, 32, 8, 128, [200, 1, 77], [17000, 9000, 300], 0),
+    "chunks_beyond_l2_d64": ("f16", 64, 16, 16, 16, [257, 40], [30000, 12345], 0),
+    "chunks_and_a_window": ("bf16", 128, 8, 8, 64, [300, 300], [20011, 5000], 3000),
+    "whole_items_beyond_l2": ("bf16", 128, 8, 8, 128, [3000], [20000], 0),
+    "whole_items_in_l2": ("f16", 64, 4, 2, 16, [5000, 33, 700], [5000, 900, 2000], 0),
+    "long_chunk_of_many_pairs": ("bf16", 64, 32, 1, 64, [900], [2000], 0),
+    "block_plan": ("bf16", 128, 8, 2, 16, [(7 * i) % 50 for i in range(90)], [60 + 13 * (i % 30) for i in range(90)], 0),
+    "block_plan_beyond_l2": ("bf16", 128, 8, 8, 64, [40] * 34, [700 + 17 * i for i in range(34)], 0),
+    "plan_kernel": ("f16", 64, 8, 1, 8, [(i * 5) % 7 for i in range(2500)], [6 + i % 20 for i in range(2500)], 0),
+    "plan_kernel_beyond_l2": ("bf16", 128, 16, 8, 64, [20] + [1] * 2100, [9000] + [30] * 2100, 0),
+    "decode_plan_kernel": ("bf16", 128, 8, 2, 16, [(i * 3) % 2 for i in range(3000)], [1 + i % 50 for i in range(3000)], 0),
+    "decode_few_long": ("bf16", 128, 16, 2, 64, [1, 1], [60000, 33], 0),
+    "few_tokens_long_window": ("f16", 128, 4, 1, 64, [8, 3], [30000, 200], 20000),
+}
+
+
+@pytest.mark.parametrize("name", BIG)
+def test_large_caches_and_batches(lib, name):
+    dtype, d, Hq, Hkv, page, T, L, window = BIG[name]
+    dtype = DTYPES[dtype]
+    n = [-(-l // page) for l in L]
+    P, width = sum(n) + 5, max(n) + 1
+    g = torch.Generator(device="cuda").manual_seed(len(name))
+    kp = torch.randn(P, Hkv, page, d, device="cuda", generator=g).to(dtype)
+    vp = torch.randn(P, Hkv, page, d, device="cuda", generator=g).to(dtype)
+    ids = torch.randperm(P, device="cuda", generator=g).to(torch.int32)
+    table = torch.full((len(L), width), -1, dtype=torch.int32)
+    idc, at = ids.cpu(), 0
+    for b, k in enumerate(n):
+        table[b, :k] = idc[at:at + k]
+        at += k
+    used = torch.zeros(P, dtype=torch.bool, device="cuda")
+    used[ids[:at].long()] = True
+    kp[~used], vp[~used] = NAN, NAN
+    table = table.cuda()
+    q = torch.randn(sum(T), Hq, d, device="cuda", generator=g).to(dtype)
+    args = (q, kp, vp, table, cu(T).cuda(), torch.tensor(L, dtype=torch.int32).cuda())
+    o, lse = lib.attn_paged(*args, max_q=max(T), window=window)
+    assert lib.attn_get_device_status()[0] == lib.ATTN_OK
+    scale = d ** -0.5
+    rows, ro, rl, pv, av = plain(q, kp, vp, table, T, L, scale, window, 24)
+    o64, l64 = o[rows].double(), lse[rows].double()
+    assert torch.equal(torch.isneginf(l64), torch.isneginf(rl))
+    # As in the oracle's bound: one rounding of the result, one of each probability (relative, or half
+    # the type's smallest step against a sum of at least 1), and scores off by (d + 8) 2^-24 sum |q_c k_c|
+    # scale < 2^-13, twice. (sum |q_c k_c| scale <= 15 for these values.)
+    half = HALF_STEP[dtype]
+    bound = half * ro.abs() * 1.01 + (half * 1.01 + 2.0 ** -12) * pv + LEAST[dtype] / 2 * av + LEAST[dtype]
+    bad = ~((o64 - ro).abs() <= bound)
+    assert not bad.any(), (rows[bad.any(-1).any(-1)].tolist(), bad.any(0).any(-1).nonzero().flatten().tolist(),
+                           bad.sum().item(), ((o64 - ro).abs() / bound).max().item())
+    seen = torch.isfinite(rl)
+    assert ((l64 - rl).abs()[seen] <= 2.0 ** -13 + 2.0 ** -18).all()
+    again, lse2 = lib.attn_paged(*args, max_q=max(T), window=window)
+    assert torch.equal(o, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_items_of_two_tiles_and_of_one_in_turns(lib, d):
+    """Many short whole items, one after another in every CTA: two tiles of rows (whose output
+    is staged), then one tile of two or three key tiles (whose groups exchange their sums)."""
+    T = [64, 20] * 700
+    L = [64 + 60 * (i % 3) for i in range(1400)]
+    L = [l if t == 64 else 300 + l % 60 for t, l in zip(T, L)]
+    kp, vp, table, _ = make_cache(L, 2, d, 64, torch.bfloat16, 41)
+    q = randn((sum(T), 8, d), torch.bfloat16, 42)
+    st = [x.cuda() for x in (q, kp, vp, table, cu(T), torch.tensor(L, dtype=torch.int32))]
+    o, lse = lib.attn_paged(*st, max_q=64)
+    rows, ro, rl, pv, av = plain(st[0], st[1], st[2], st[3], T, L, d ** -0.5, 0, 3)
+    half = HALF_STEP[torch.bfloat16]
+    assert ((o[rows].double() - ro).abs() <= half * ro.abs() * 1.01 + (half * 1.01 + 2.0 ** -12) * pv + 2.0 ** -30).all()
+    assert ((lse[rows].double() - rl).abs() <= 2.0 ** -13 + 2.0 ** -18).all()
+    for _ in range(20):
+        again, lse2 = lib.attn_paged(*st, max_q=64)
+        assert torch.equal(o, again) and torch.equal(lse, lse2)
+
+
 def test_binding_refusals(lib):
     kp, vp, table, _ = make_cache([20], 2, 64, 16, torch.bfloat16, 1)
     kg, vg, tg = kp.cuda(), vp.cuda(), table.cuda()
