@@ -231,6 +231,13 @@ __device__ __forceinline__ int first_key(int len, int window) {
   return (window > 0 && len > window) ? len - window : 0;
 }
 
+// CTAs that the tiles (or cost positions) are dealt to. PAGED: not more than
+// there are, so that each of them has one (the gather need not ask).
+template <bool PAGED>
+__host__ __device__ __forceinline__ int ctas_for(int nc, long long total) {
+  return PAGED && total < nc ? static_cast<int>(total) : nc;
+}
+
 // Length, rows and first key of sequence b. PAGED: T new tokens at rows q0 on,
 // the first of which sees back to key k0; without new tokens nothing is read.
 struct SeqKeys {
@@ -347,9 +354,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_decode_plan_kernel(const PP
       // CTAs of the equal tile ranges whose first tile lies in this sequence:
       // CTA c starts at tile c * T / nc.
       const long long span = static_cast<long long>(Hkv) * nt;
-      for (long long c = (l_run * nc + T - 1) / T; c < nc && c * T / nc < l_run + span; ++c) {
-        const long long lo = c * T / nc;
-        if (lo >= (c + 1) * T / nc) continue;  // an empty range: the CTA does nothing
+      const int n_ctas = ctas_for<PAGED>(nc, T);
+      for (long long c = (l_run * n_ctas + T - 1) / T; c < n_ctas && c * T / n_ctas < l_run + span; ++c) {
+        const long long lo = c * T / n_ctas;
+        if (lo >= (c + 1) * T / n_ctas) continue;  // an empty range: the CTA does nothing
         const int r = static_cast<int>(lo - l_run);
         p.starts[c] = make_int4(b, r / nt, r % nt, 0);
       }
@@ -374,9 +382,15 @@ __device__ __forceinline__ long long segment_start(const PParams& p, long long s
   return p.tile_off[b] + static_cast<long long>(g) * nt;
 }
 
-__device__ __forceinline__ Range cta_range(const PParams& p, int c, int nc) {
+template <bool PAGED>
+__device__ __forceinline__ Range cta_range(const PParams& p, int c, int all) {
   const long long T = p.tile_off[p.B];
+  const int nc = ctas_for<PAGED>(all, T);
   Range r;
+  if (PAGED && c >= nc) {
+    r.lo = r.hi = 0;
+    return r;
+  }
   if (p.seg_aligned) {
     const long long S = static_cast<long long>(p.B) * p.Hkv;
     r.lo = segment_start(p, c * S / nc, T);
@@ -687,7 +701,71 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
   griddep_launch_dependents();
   Range rg;
   Cursor<PAGED> cur;
-  if (p.inline_plan) {
+  bool planned = false;
+  if constexpr (PAGED) {
+    // Up to 32 sequences: every warp plans for itself, a lane per sequence,
+    // without a barrier (the same positions as below; a kernel's start runs on
+    // cold caches, so its code and its steps are kept few: 3,300 -> 2,000
+    // cycles).
+    if (p.inline_plan && p.B <= 32) {
+      planned = true;
+      SeqKeys sk{0, 0, 0, 0, 0};
+      if (lane < p.B) sk = seq_keys<true>(p, lane);
+      const int wc = p.wcost, span = p.Hkv * sk.nt, kspan = sk.nt > 0 ? span + wc * p.Hkv : 0;
+      int xs = span, xk = kspan;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int ys = __shfl_up_sync(0xffffffffu, xs, o), yk = __shfl_up_sync(0xffffffffu, xk, o);
+        if (lane >= o) {
+          xs += ys;
+          xk += yk;
+        }
+      }
+      const int T_all = __shfl_sync(0xffffffffu, xs, 31), C_all = __shfl_sync(0xffffffffu, xk, 31);
+      if (warp == 0 && lane < p.B) {
+        if (c == 0) {
+          const_cast<int*>(p.tile_off)[lane] = xk - kspan;
+          if (lane == 0) const_cast<int*>(p.tile_off)[p.B] = C_all;
+          paged::check_seq(p.cu_q, p.seqlens, lane, p.total_q, p.max_q, p.cache.capacity());
+        }
+        if (sk.nt == 0 && lane % static_cast<int>(gridDim.x) == c) write_empty<D, true>(p, lane);
+      }
+      // The tile at or after a cost position: its sequence, and its rank there.
+      auto tile_at = [&](long long x, int& b) {
+        b = __ffs(__ballot_sync(0xffffffffu, xk > x)) - 1;
+        const int nt = __shfl_sync(0xffffffffu, sk.nt, b);
+        const int r = static_cast<int>(x) - __shfl_sync(0xffffffffu, xk - kspan, b);
+        const int g = r / (nt + wc);
+        return g * nt + max(r - g * (nt + wc) - wc, 0);
+      };
+      const int nc = ctas_for<true>(gridDim.x, C_all);
+      rg.lo = rg.hi = 0;
+      if (c < nc) {
+        const long long x_lo = div_nonneg(static_cast<long long>(c) * C_all, nc);
+        const long long x_hi = div_nonneg((c + 1LL) * C_all, nc);
+        int b, bh;
+        const int r = tile_at(x_lo, b);
+        rg.lo = __shfl_sync(0xffffffffu, xs - span, b) + r;
+        rg.hi = T_all;
+        if (x_hi < C_all) {
+          const int rh = tile_at(x_hi, bh);
+          rg.hi = __shfl_sync(0xffffffffu, xs - span, bh) + rh;
+        }
+        cur.b = b;
+        cur.len = __shfl_sync(0xffffffffu, sk.len, b);
+        cur.k0 = __shfl_sync(0xffffffffu, sk.k0, b);
+        cur.nt = __shfl_sync(0xffffffffu, sk.nt, b);
+        cur.q0 = __shfl_sync(0xffffffffu, sk.q0, b);
+        cur.T = __shfl_sync(0xffffffffu, sk.T, b);
+        cur.g = r / cur.nt;
+        cur.i = r - cur.g * cur.nt;
+        cur.tok = 0;  // (packed caches only)
+      }
+    }
+  }
+  if (planned) {
+    // done
+  } else if (p.inline_plan) {
     // Prefix sums over the sequences in this CTA (small batches): the total
     // tile count, this CTA's range and its first tile, without a plan kernel.
     // Cost positions: each non-empty segment takes wcost positions, then one
@@ -761,8 +839,10 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
     long long t_run = xk - tok + (warp > 0 ? wsum[2 * (warp - 1) + 1] : 0);
     long long k_run = l_run + wseg * (t_run >> 48);
     t_run &= kSeqOne - 1;
-    const long long x_lo = div_nonneg(c * C_all, gridDim.x);
-    const long long x_hi = div_nonneg((c + 1) * C_all, gridDim.x);
+    const int nc = ctas_for<PAGED>(gridDim.x, C_all);
+    // (a CTA beyond them begins behind the last position)
+    const long long x_lo = c < nc ? div_nonneg(c * C_all, nc) : C_all;
+    const long long x_hi = c < nc ? div_nonneg((c + 1) * C_all, nc) : C_all;
     for (int b = b0; b < b1; ++b) {
       const SeqKeys sk = seq_keys<PAGED>(p, b);
       const int len = sk.len, nt = sk.nt;
@@ -811,7 +891,7 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
       cur.tok = start[2];
     }
   } else {
-    rg = cta_range(p, c, gridDim.x);
+    rg = cta_range<PAGED>(p, c, gridDim.x);
     if (rg.hi > rg.lo) {
       if (p.seg_aligned) {
         cur.seek(p, rg.lo);
@@ -1314,7 +1394,7 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
 // PAGED: one warp per (sequence, KV head, row of its R), the rows being (new
 // token, head of the group).
 template <int D, typename T, bool PAGED = false>
-__global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p, int nc) {
+__global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p, int all) {
   constexpr int EPL = D / 32;  // output elements per lane
   griddep_wait();  // the stream kernel's partials and outputs are visible after this
   const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
@@ -1331,9 +1411,15 @@ __global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p
   // at tile_off[b] + g (nt + wcost) + wcost + i.
   const int w = p.wcost;
   const int span = p.tile_off[b + 1] - p.tile_off[b];
+  [[maybe_unused]] SeqKeys sk{0, 0, 0, 0, 0};
+  if constexpr (PAGED) {
+    sk = seq_keys<true>(p, b);  // (its loads go along with the tile offsets')
+    if (hh >= sk.T * p.G) return;  // no such row: its slot was not written
+  }
   if (span == 0 || p.seg_aligned) return;
   const int nt = span / p.Hkv - w;
   const long long T_all = p.tile_off[p.B];  // all cost positions
+  const int nc = ctas_for<PAGED>(all, T_all);
   const long long a = p.tile_off[b] + static_cast<long long>(g) * (nt + w) + w;
   const int c0 = cta_of(a, T_all, nc);
   const int c1 = cta_of(a + nt - 1, T_all, nc);
@@ -1344,7 +1430,7 @@ __global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p
   // partials of the first kMaxP CTAs are all loaded before any is used, so
   // their loads overlap; a running maximum then folds them (and, for longer
   // cuts, the rest) in.
-  const bool all_have = T_all >= nc;
+  const bool all_have = PAGED || T_all >= nc;
   auto has_tiles = [&](int cc) {
     return all_have || div_nonneg(cc * T_all, nc) < div_nonneg((cc + 1) * T_all, nc);
   };
@@ -1397,8 +1483,6 @@ __global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p
   long long orow = row;
   int cols = D;
   if constexpr (PAGED) {
-    const SeqKeys sk = seq_keys<true>(p, b);
-    if (hh >= sk.T * p.G) return;  // no such row: its slot was not written
     const int tok = hh / p.G;
     orow = (static_cast<long long>(sk.q0) + tok) * p.Hq + g * p.G + hh - tok * p.G;
     cols = p.cache.d;
