@@ -148,6 +148,16 @@ int launch_paged(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap
   return rc;
 }
 
+// Cost of a segment's start, in tiles, when the CTAs of the paged decode pass
+// share out the work. Measured on B200 with 0 / 1 / 2 / 3 / 4: the ragged batch
+// of 64 x 1K-8K tokens 199 / 194 / 197 / 194 / 194 us, 256 sequences of 50-600
+// tokens 116 / 91 / 87 / 88 / 90 us, 61 sequences under a window of 1006
+// tokens 48 / 42 / 37 / 36 / 37 us, 1 to 4 new tokens over 500-4096 129 / 117 /
+// 109 / 106 / 105 us; groups of 16 and 32 heads as before.
+#ifndef ETA_PAGED_SEG_COST
+#define ETA_PAGED_SEG_COST 3
+#endif
+
 // Few rows of a KV head (max_q G <= 32): the persistent decode pass, whose
 // products have the keys on the tensor core's long side, over pages. Batches whose
 // tiles could not be counted in 32 bits take the other kernel.
@@ -171,10 +181,7 @@ int paged_decode_run(const void* q, long long q_stride, const paged::Cache& c, c
   p.window = window;
   p.inline_plan = B <= ETA_DECODE_INLINE_PLAN_MAX_B ? 1 : 0;
   p.R = max_q * G;
-  p.wcost = !p.inline_plan ? 0
-            : p.R <= 8     ? 0
-            : p.R <= 16    ? ETA_DECODE_PS_SEG_COST16
-                           : ETA_DECODE_PS_SEG_COST32;
+  p.wcost = p.inline_plan ? ETA_PAGED_SEG_COST : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_ns = kDefaultWaitNs;
   p.cu_q = cu_q;

@@ -131,14 +131,13 @@ struct alignas(16) Start {
   int i;           // step of the item
   int chunk;       // the first chunk CTA of the item, or of the next that has one
   int pad;
-  long long rest;  // rests before the item's
+  long long rest;  // positions of the rests before the item's
 };
 
 // The plan, in device memory.
 struct Head {
-  long long steps;  // of all items
-  long long w;      // steps of a CTA
-  long long rest;   // steps that are not in chunks
+  long long w;      // steps of a chunk, positions of a CTA that takes rests
+  long long rest;   // positions of all rests
   int chunks;       // CTAs that take a chunk: 0 .. chunks - 1; the rests follow
   int ctas;         // CTAs with work
 };
@@ -208,6 +207,17 @@ __device__ __forceinline__ int chunks_of(int n, long long w, bool chunked) {
 // A range of fewer steps than this is not worth a CTA of its own.
 constexpr int kMinSteps = 2;
 
+// What beginning an item costs a CTA, in steps: loading its queries, and its
+// end (the last product, the output). The rests are dealt out by their steps
+// and this for each.
+#ifndef ETA_PAGED_ITEM_COST
+#define ETA_PAGED_ITEM_COST 2
+#endif
+constexpr int kItemCost = ETA_PAGED_ITEM_COST;
+
+// Positions of an item's rest of r steps.
+__device__ __forceinline__ int rest_cost(int r) { return r > 0 ? r + kItemCost : 0; }
+
 // Sums over a block of (a, b), which every thread gets; `red` holds 2 THREADS / 32 words.
 template <int THREADS>
 __device__ __forceinline__ void block_sum(long long& a, long long& b, long long* red) {
@@ -247,7 +257,7 @@ __device__ __forceinline__ Head make_plan(const Params& p, long long* rest_at, i
   for (int b = b_first; b < p.B; b += b_step) {
     const Seq s = load_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
     const int n = pairs_of(p, s.T);
-    for (int i = i_first; i < n; i += i_step) steps += span_of(p, s, i).n;
+    for (int i = i_first; i < n; i += i_step) steps += span_of(p, s, i).n + kItemCost;
     if (i_first == 0) {
       keys += s.T > 0 ? s.L : 0;
       if (check) check_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
@@ -255,10 +265,10 @@ __device__ __forceinline__ Head make_plan(const Params& p, long long* rest_at, i
   }
   block_sum<THREADS>(steps, keys, red);
   Head h;
-  h.steps = steps * p.Hkv;
-  const long long want = div_pos(h.steps + kMinSteps - 1, kMinSteps);
-  const int busy = static_cast<int>(want < p.nc ? want : p.nc);
-  h.w = busy > 0 ? div_pos(h.steps + busy - 1, busy) : 1;
+  steps *= p.Hkv;  // (with what each item's beginning costs)
+  const long long want = div_pos(steps, kMinSteps + kItemCost);
+  const int busy = static_cast<int>(want < p.nc ? (want > 0 ? want : 1) : p.nc);
+  h.w = max(div_pos(steps + busy - 1, busy), 1LL);
   // Keys and values beyond half of L2 will not stay in it between two CTAs
   // that come by at different times.
   const bool chunked = keys * p.Hkv * p.d * 4 > p.l2_bytes / 2;
@@ -270,7 +280,7 @@ __device__ __forceinline__ Head make_plan(const Params& p, long long* rest_at, i
     for (int i = i_first; i < n; i += i_step) {
       const int k = span_of(p, s, i).n, f = chunks_of(k, h.w, chunked);
       chunks += f;
-      rest += k - f * h.w;
+      rest += rest_cost(static_cast<int>(k - f * h.w));
     }
     if (wide) {
 #pragma unroll
@@ -371,7 +381,7 @@ __device__ __forceinline__ Start plan_find(const Params& p, const Head& h, const
   for (int i0 = 0; i0 < n; i0 += 32) {
     const int k = i0 + lane < n ? span_of(p, s, i0 + lane).n : 0;
     const int f = chunks_of(k, h.w, chunked);
-    const int rr = static_cast<int>(k - f * h.w);  // (32 spans stay below 2^31)
+    const int rr = rest_cost(static_cast<int>(k - f * h.w));  // (32 spans stay below 2^31)
     int x = rr, y = f;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -390,7 +400,8 @@ __device__ __forceinline__ Start plan_find(const Params& p, const Head& h, const
       st.chunk += __shfl_sync(0xffffffffu, y - f, l);
       const int before = __shfl_sync(0xffffffffu, mine ? y - f : x - rr, l);
       const int fl = __shfl_sync(0xffffffffu, f, l);
-      st.i = static_cast<int>(mine ? (r - before) * h.w : fl * h.w + (r - before));
+      st.i = static_cast<int>(mine ? (r - before) * h.w
+                                   : fl * h.w + max(static_cast<int>(r - before) - kItemCost, 0));
       break;
     }
     r -= __shfl_sync(0xffffffffu, mine ? y : x, 31);
@@ -412,13 +423,13 @@ __device__ __forceinline__ bool plan_warp(const Params& p, int c, int lane, Head
   int mine = 0;
   float keys = s.T > 0 ? static_cast<float>(s.L) : 0.f;
   if (p.max_pairs <= 32) {
-    for (int i = 0; i < n; ++i) mine += span_of(p, s, i).n;
+    for (int i = 0; i < n; ++i) mine += span_of(p, s, i).n + kItemCost;
   } else {
     for (int b = 0; b < p.B; ++b) {  // long chunks: the lanes share a sequence's pairs
       const Seq t{0, __shfl_sync(0xffffffffu, s.T, b), __shfl_sync(0xffffffffu, s.L, b)};
       const int m = pairs_of(p, t.T);
       int sum = 0;
-      for (int i = lane; i < m; i += 32) sum += span_of(p, t, i).n;
+      for (int i = lane; i < m; i += 32) sum += span_of(p, t, i).n + kItemCost;
       sum = __reduce_add_sync(0xffffffffu, sum);
       if (lane == b) mine = sum;
     }
@@ -433,10 +444,10 @@ __device__ __forceinline__ bool plan_warp(const Params& p, int c, int lane, Head
   }
   if (keys * p.Hkv * p.d * 4.f > static_cast<float>(p.l2_bytes / 2)) return false;
   const unsigned steps = __shfl_sync(0xffffffffu, x, 31);
-  const unsigned want = (steps + kMinSteps - 1) / kMinSteps;
-  const unsigned busy = min(want, static_cast<unsigned>(p.nc));
-  const unsigned w = busy > 0 ? (steps + busy - 1) / busy : 1;
-  h.steps = h.rest = steps;
+  const unsigned busy =
+      min(max(steps / (kMinSteps + kItemCost), 1u), static_cast<unsigned>(p.nc));
+  const unsigned w = max((steps + busy - 1) / busy, 1u);
+  h.rest = steps;
   h.w = w;
   h.chunks = 0;
   h.ctas = static_cast<int>((steps + w - 1) / w);
@@ -455,7 +466,7 @@ __device__ __forceinline__ bool plan_warp(const Params& p, int c, int lane, Head
   st.pair = st.i = 0;
   const int m = pairs_of(p, t.T);
   for (int i0 = 0; i0 < m; i0 += 32) {
-    const int k = i0 + lane < m ? span_of(p, t, i0 + lane).n : 0;
+    const int k = i0 + lane < m ? span_of(p, t, i0 + lane).n + kItemCost : 0;
     int y = k;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -466,7 +477,7 @@ __device__ __forceinline__ bool plan_warp(const Params& p, int c, int lane, Head
     if (over != 0) {
       const int l = __ffs(over) - 1, before = __shfl_sync(0xffffffffu, y - k, l);
       st.pair = i0 + l;
-      st.i = static_cast<int>(r) - before;
+      st.i = max(static_cast<int>(r) - before - kItemCost, 0);
       st.rest += before;
       break;
     }
@@ -513,12 +524,16 @@ struct Walk {
     n = sp.n;
     first = w > 0 && n >= w ? n - static_cast<int>(static_cast<unsigned>(n) % static_cast<unsigned>(w)) : 0;
   }
-  __device__ __forceinline__ void piece(int from) {
+  // False: the range ends within what the item's beginning costs.
+  __device__ __forceinline__ bool piece(int from, int cost) {
+    left -= cost;
+    if (left <= 0) return false;
     i0 = from;
     i1 = min(n, i0 + left);
     left -= i1 - i0;
     rot = i0 == first && i1 == n ? done % (n - first) : 0;
     done += i1 - i0;
+    return true;
   }
   __device__ __forceinline__ void start(const Params& p, const Head& h, const Start& st, int c) {
     b = st.b, g = st.g, pair = st.pair, chunk = st.chunk;
@@ -531,7 +546,10 @@ struct Walk {
     more = 1;
     s = load_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
     item(p);
-    piece(st.i);
+    // (a range may begin within the positions before an item's first step)
+    const bool rests = c >= h.chunks;
+    const long long into = (c - h.chunks) * h.w - st.rest;
+    more = piece(st.i, rests && into < kItemCost ? static_cast<int>(kItemCost - into) : 0) ? 1 : 0;
   }
   __device__ __forceinline__ void next(const Params& p) {
     more = 0;
@@ -550,8 +568,7 @@ struct Walk {
       }
       item(p);
     } while (first == n);
-    piece(first);
-    more = 1;
+    more = piece(first, kItemCost) ? 1 : 0;
   }
   __device__ __forceinline__ int steps() const { return i1 - i0; }
   __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == n; }
@@ -573,6 +590,13 @@ __device__ __forceinline__ bool walk_on(Walk& w, const Params& p, int lane) {
   if (lane == 0) w.next(p);
   __syncwarp();
   return w.more != 0;
+}
+
+// 32 bytes to a 32-byte-aligned address.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 template <int D, typename T>
@@ -1109,38 +1133,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const float l2 = l > 0.f ? m + lg2_approx(l) : -INFINITY;
         if (w.whole()) {
-          // 64 columns at a time through the warp's staging rows, so that a
-          // store instruction writes whole lines: 16-byte chunk u of row q
-          // sits at chunk u ^ (q % 8).
-          uint8_t* stg = smem + C::kStgOff + warp * C::kStgWarpBytes;
+          // Each thread writes its own row, a 32-byte sector at a time. (Through
+          // shared memory, in whole lines, it took twice as long.)
           const size_t orow = (static_cast<size_t>(w.s.q0) + tok) * p.Hq + w.g * p.G + r % p.G;
-          const long long my = row_ok ? static_cast<long long>(orow) : -1;
+          T* dst = reinterpret_cast<T*>(p.o) + orow * p.d;
+          const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
 #pragma unroll
-          for (int half = 0; half < D / 64; ++half) {
-            __syncwarp();
+          for (int col = 0; col < D; col += 32) {
+            float f[32];
+            columns(col, f);
+            if (!row_ok) continue;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float f[32];
-              columns(half * 64 + h * 32, f);
+            for (int u = 0; u < 2; ++u) {
+              uint32_t v[8];
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                uint4 v;
-                v.x = prefill::pack2<T>(f[8 * u], f[8 * u + 1]);
-                v.y = prefill::pack2<T>(f[8 * u + 2], f[8 * u + 3]);
-                v.z = prefill::pack2<T>(f[8 * u + 4], f[8 * u + 5]);
-                v.w = prefill::pack2<T>(f[8 * u + 6], f[8 * u + 7]);
-                *reinterpret_cast<uint4*>(stg + lane * 128 + (((h * 4 + u) ^ (lane & 7)) << 4)) = v;
+              for (int e = 0; e < 8; ++e)
+                v[e] = prefill::pack2<T>(f[16 * u + 2 * e], f[16 * u + 2 * e + 1]);
+              const int at = col + 16 * u;
+              if (sectors && at + 16 <= p.d) {
+                st_global_32(dst + at, v);
+              } else {
+                if (at < p.d) *reinterpret_cast<uint4*>(dst + at) = make_uint4(v[0], v[1], v[2], v[3]);
+                if (at + 8 < p.d)
+                  *reinterpret_cast<uint4*>(dst + at + 8) = make_uint4(v[4], v[5], v[6], v[7]);
               }
-            }
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int q = k * 4 + (lane >> 3), u = lane & 7;
-              const long long to = __shfl_sync(0xffffffffu, my, q);
-              const uint4 v = *reinterpret_cast<const uint4*>(stg + q * 128 + ((u ^ (q & 7)) << 4));
-              const int col = half * 64 + u * 8;
-              if (to >= 0 && col < p.d)
-                *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.o) + to * p.d + col) = v;
             }
           }
           if (row_ok && p.lse != nullptr) p.lse[orow] = l2 * 0.69314718055994531f;
@@ -1204,12 +1220,14 @@ __global__ void __launch_bounds__(256) attn_paged_gather_kernel(const Params p) 
   const int rest = static_cast<int>(n - f * h.w);
   if (has_chunks) {
     if (nx.i != 0 || (f == 1 && rest == 0)) return;  // not the first chunk, or the whole item
-  } else if (f > 0 || nx.i == 0 || nx.i > h.w) {
-    return;  // chunks' business, a boundary between items, or begun before c
+  } else if (f > 0 || nx.i == 0) {
+    return;  // chunks' business, or a boundary between items
   }
   // Its partials: chunks c .. c + f - 1, then the CTAs q0 .. q1 of the rest.
-  const int q0 = h.chunks + static_cast<int>(div_pos(nx.rest, h.w));
-  const int q1 = rest > 0 ? h.chunks + static_cast<int>(div_pos(nx.rest + rest - 1, h.w)) : q0 - 1;
+  const int q0 = h.chunks + static_cast<int>(div_pos(nx.rest + kItemCost, h.w));
+  const int q1 = rest > 0 ? h.chunks + static_cast<int>(div_pos(nx.rest + kItemCost + rest - 1, h.w))
+                          : q0 - 1;
+  if (!has_chunks && q0 != c) return;  // begun before c
   const int parts = f + q1 - q0 + 1;
   auto slot_of = [&](int k) {
     if (k < f) return c + k;
