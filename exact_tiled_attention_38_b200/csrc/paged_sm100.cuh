@@ -110,7 +110,7 @@ struct Cfg {
   // times. (Its own place: its neighbours may still be storing the last piece's.)
   static constexpr int kXOff = kStgOff + 4 * kStgWarpBytes;
   static constexpr int kWalkOff = kCtlOff + 64;  // each warp's way through the range
-  static constexpr int kSmemBytes = kWalkOff + 10 * 96 + 1024;  // + runtime 1024-byte alignment
+  static constexpr int kSmemBytes = kWalkOff + 10 * 104 + 1024;  // + runtime 1024-byte alignment
   static constexpr uint32_t kTmemCols = 512;
   static constexpr bool kOwnP = D == 64;  // P in columns of its own, else over S from column 64 on
   __host__ __device__ static constexpr uint32_t s_col(int t) { return kOwnP ? 256u * t : BN * t; }
@@ -136,8 +136,8 @@ struct alignas(16) Start {
 
 // The plan, in device memory.
 struct Head {
-  long long w;      // steps of a chunk, positions of a CTA that takes rests
   long long rest;   // positions of all rests
+  int w;            // cost of a chunk, positions of a CTA that takes rests
   int chunks;       // CTAs that take a chunk: 0 .. chunks - 1; the rests follow
   int ctas;         // CTAs with work
 };
@@ -199,24 +199,36 @@ __device__ __forceinline__ long long div_pos(long long n, long long d) {
   return n / d;
 }
 
-// Chunks of w steps in an item of n (0: the item goes to the rests whole).
-__device__ __forceinline__ int chunks_of(int n, long long w, bool chunked) {
-  return chunked && n >= w ? static_cast<int>(static_cast<unsigned>(n) / static_cast<unsigned>(w)) : 0;
+// Costs are counted in thirds of a pair's step. A step with one tile of rows
+// takes two of them (measured at d = 128: 3,550 cycles against 2,350, which is
+// what its keys and values take to arrive).
+constexpr int kPairCost = 3, kSingleCost = 2;
+__device__ __forceinline__ int step_cost(const Params& p, int T, int pair) {
+  return pair * NQT * p.tt + p.tt < T ? kPairCost : kSingleCost;
 }
 
-// A range of fewer steps than this is not worth a CTA of its own.
-constexpr int kMinSteps = 2;
-
-// What beginning an item costs a CTA, in steps: loading its queries, and its
-// end (the last product, the output). The rests are dealt out by their steps
-// and this for each.
+// What beginning an item costs a CTA: loading its queries, and its end (the
+// last product, the output). Measured with none / one / two / three / four
+// steps on B200: 16 chunks of 128-512 tokens over 600-4000 275 / 251 / 242 /
+// 237 / 224 us, 8K tokens 591 / 556 / 515 / 515 / 529, the mixed batch of 9
+// 58.6 / 55.2 / 55.4 / 56.1 / 56.5.
 #ifndef ETA_PAGED_ITEM_COST
 #define ETA_PAGED_ITEM_COST 2
 #endif
-constexpr int kItemCost = ETA_PAGED_ITEM_COST;
+constexpr int kItemCost = ETA_PAGED_ITEM_COST * kPairCost;
+// A range of less is not worth a CTA of its own. (It also holds a step's
+// beginning wherever it lies.)
+constexpr int kMinCost = 2 * kPairCost + kItemCost;
 
-// Positions of an item's rest of r steps.
-__device__ __forceinline__ int rest_cost(int r) { return r > 0 ? r + kItemCost : 0; }
+// Steps of a chunk, and chunks of an item of n steps (0: all of it goes to the rests).
+__device__ __forceinline__ int chunk_steps(int w, int g) { return (w + g - 1) / g; }
+__device__ __forceinline__ int chunks_of(int n, int wc, bool chunked) {
+  return chunked && n >= wc ? static_cast<int>(static_cast<unsigned>(n) / static_cast<unsigned>(wc)) : 0;
+}
+
+// Positions of an item's rest of r steps: what its beginning costs, then the
+// steps. A CTA takes the steps that begin in its range.
+__device__ __forceinline__ int rest_cost(int r, int g) { return r > 0 ? r * g + kItemCost : 0; }
 
 // Sums over a block of (a, b), which every thread gets; `red` holds 2 THREADS / 32 words.
 template <int THREADS>
@@ -257,7 +269,8 @@ __device__ __forceinline__ Head make_plan(const Params& p, long long* rest_at, i
   for (int b = b_first; b < p.B; b += b_step) {
     const Seq s = load_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
     const int n = pairs_of(p, s.T);
-    for (int i = i_first; i < n; i += i_step) steps += span_of(p, s, i).n + kItemCost;
+    for (int i = i_first; i < n; i += i_step)
+      steps += rest_cost(span_of(p, s, i).n, step_cost(p, s.T, i));
     if (i_first == 0) {
       keys += s.T > 0 ? s.L : 0;
       if (check) check_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
@@ -265,10 +278,10 @@ __device__ __forceinline__ Head make_plan(const Params& p, long long* rest_at, i
   }
   block_sum<THREADS>(steps, keys, red);
   Head h;
-  steps *= p.Hkv;  // (with what each item's beginning costs)
-  const long long want = div_pos(steps, kMinSteps + kItemCost);
+  steps *= p.Hkv;
+  const long long want = div_pos(steps, kMinCost);
   const int busy = static_cast<int>(want < p.nc ? (want > 0 ? want : 1) : p.nc);
-  h.w = max(div_pos(steps + busy - 1, busy), 1LL);
+  h.w = static_cast<int>(max(div_pos(steps + busy - 1, busy), 1LL));
   // Keys and values beyond half of L2 will not stay in it between two CTAs
   // that come by at different times.
   const bool chunked = keys * p.Hkv * p.d * 4 > p.l2_bytes / 2;
@@ -278,9 +291,10 @@ __device__ __forceinline__ Head make_plan(const Params& p, long long* rest_at, i
     long long rest = 0;
     int chunks = 0;
     for (int i = i_first; i < n; i += i_step) {
-      const int k = span_of(p, s, i).n, f = chunks_of(k, h.w, chunked);
+      const int k = span_of(p, s, i).n, g = step_cost(p, s.T, i), wc = chunk_steps(h.w, g);
+      const int f = chunks_of(k, wc, chunked);
       chunks += f;
-      rest += rest_cost(static_cast<int>(k - f * h.w));
+      rest += rest_cost(k - f * wc, g);
     }
     if (wide) {
 #pragma unroll
@@ -354,7 +368,7 @@ __device__ __forceinline__ Head make_plan(const Params& p, long long* rest_at, i
 __device__ __forceinline__ Start plan_find(const Params& p, const Head& h, const long long* rest_at,
                                            const int* chunk_at, int c, int lane) {
   const bool chunked = h.chunks > 0, mine = c < h.chunks;
-  const long long at = mine ? c : (c - h.chunks) * h.w;  // among the chunks, or the rests
+  const long long at = mine ? c : static_cast<long long>(c - h.chunks) * h.w;  // among the chunks, or the rests
   int lo = 0, hi = p.B - 1;  // the last sequence that begins at or before `at`
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -380,8 +394,9 @@ __device__ __forceinline__ Start plan_find(const Params& p, const Head& h, const
   const int n = pairs_of(p, s.T);
   for (int i0 = 0; i0 < n; i0 += 32) {
     const int k = i0 + lane < n ? span_of(p, s, i0 + lane).n : 0;
-    const int f = chunks_of(k, h.w, chunked);
-    const int rr = rest_cost(static_cast<int>(k - f * h.w));  // (32 spans stay below 2^31)
+    const int g = step_cost(p, s.T, i0 + lane), wc = chunk_steps(h.w, g);
+    const int f = chunks_of(k, wc, chunked);
+    const int rr = rest_cost(k - f * wc, g);  // (32 spans stay below 2^31)
     int x = rr, y = f;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -399,9 +414,8 @@ __device__ __forceinline__ Start plan_find(const Params& p, const Head& h, const
       st.rest += __shfl_sync(0xffffffffu, x - rr, l);
       st.chunk += __shfl_sync(0xffffffffu, y - f, l);
       const int before = __shfl_sync(0xffffffffu, mine ? y - f : x - rr, l);
-      const int fl = __shfl_sync(0xffffffffu, f, l);
-      st.i = static_cast<int>(mine ? (r - before) * h.w
-                                   : fl * h.w + max(static_cast<int>(r - before) - kItemCost, 0));
+      // (a rest: the walk finds the step from the range's position)
+      st.i = mine ? static_cast<int>(r - before) * __shfl_sync(0xffffffffu, wc, l) : 0;
       break;
     }
     r -= __shfl_sync(0xffffffffu, mine ? y : x, 31);
@@ -420,16 +434,24 @@ __device__ __forceinline__ bool plan_warp(const Params& p, int c, int lane, Head
   Seq s{0, 0, 0};
   if (lane < p.B) s = load_seq(p.cu_q, p.lens, lane, p.total_q, p.max_q, p.capacity());
   const int n = pairs_of(p, s.T);
-  int mine = 0;
+  int mine = 0, longest = 0;
   float keys = s.T > 0 ? static_cast<float>(s.L) : 0.f;
   if (p.max_pairs <= 32) {
-    for (int i = 0; i < n; ++i) mine += span_of(p, s, i).n + kItemCost;
+    for (int i = 0; i < n; ++i) {
+      const int k = span_of(p, s, i).n;
+      mine += rest_cost(k, step_cost(p, s.T, i));
+      longest = max(longest, k);
+    }
   } else {
     for (int b = 0; b < p.B; ++b) {  // long chunks: the lanes share a sequence's pairs
       const Seq t{0, __shfl_sync(0xffffffffu, s.T, b), __shfl_sync(0xffffffffu, s.L, b)};
       const int m = pairs_of(p, t.T);
       int sum = 0;
-      for (int i = lane; i < m; i += 32) sum += span_of(p, t, i).n + kItemCost;
+      for (int i = lane; i < m; i += 32) {
+        const int k = span_of(p, t, i).n;
+        sum += rest_cost(k, step_cost(p, t.T, i));
+        longest = max(longest, k);
+      }
       sum = __reduce_add_sync(0xffffffffu, sum);
       if (lane == b) mine = sum;
     }
@@ -442,13 +464,14 @@ __device__ __forceinline__ bool plan_warp(const Params& p, int c, int lane, Head
     keys += __shfl_xor_sync(0xffffffffu, keys, o);
     if (lane >= o) x += y;
   }
-  if (keys * p.Hkv * p.d * 4.f > static_cast<float>(p.l2_bytes / 2)) return false;
   const unsigned steps = __shfl_sync(0xffffffffu, x, 31);
-  const unsigned busy =
-      min(max(steps / (kMinSteps + kItemCost), 1u), static_cast<unsigned>(p.nc));
+  const unsigned busy = min(max(steps / kMinCost, 1u), static_cast<unsigned>(p.nc));
   const unsigned w = max((steps + busy - 1) / busy, 1u);
+  if (keys * p.Hkv * p.d * 4.f > static_cast<float>(p.l2_bytes / 2) &&
+      __reduce_max_sync(0xffffffffu, longest) >= chunk_steps(w, kPairCost))
+    return false;  // there are chunks
   h.rest = steps;
-  h.w = w;
+  h.w = static_cast<int>(w);
   h.chunks = 0;
   h.ctas = static_cast<int>((steps + w - 1) / w);
   if (c >= h.ctas) return true;
@@ -466,7 +489,8 @@ __device__ __forceinline__ bool plan_warp(const Params& p, int c, int lane, Head
   st.pair = st.i = 0;
   const int m = pairs_of(p, t.T);
   for (int i0 = 0; i0 < m; i0 += 32) {
-    const int k = i0 + lane < m ? span_of(p, t, i0 + lane).n + kItemCost : 0;
+    const int k = i0 + lane < m
+                      ? rest_cost(span_of(p, t, i0 + lane).n, step_cost(p, t.T, i0 + lane)) : 0;
     int y = k;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -477,7 +501,6 @@ __device__ __forceinline__ bool plan_warp(const Params& p, int c, int lane, Head
     if (over != 0) {
       const int l = __ffs(over) - 1, before = __shfl_sync(0xffffffffu, y - k, l);
       st.pair = i0 + l;
-      st.i = max(static_cast<int>(r) - before - kItemCost, 0);
       st.rest += before;
       break;
     }
@@ -503,16 +526,18 @@ __global__ void __launch_bounds__(kPlanThreads) attn_paged_plan_kernel(const Par
 // shared memory (in registers it would push the softmax's scores out): lane 0
 // moves it on, the others read it.
 struct Walk {
-  int b, g, pair;
+  int b, head, pair;
   int i0, i1, n;   // steps [i0, i1) of the item's n
   int first;       // the item's first step outside its chunks
   int lo;          // its first key tile
   int rot;         // the piece begins at its step rot and wraps around
   int chunk;       // the item's first chunk CTA (if it has chunks)
   int more;        // this is a piece (0: the range has ended)
-  int w;           // steps of a chunk (0: no item has any)
-  int left;        // steps of the range behind this piece
-  int done;        // and up to its end
+  int w;           // cost of a chunk (0: no item has any)
+  int wc;          // and its steps
+  int g;           // cost of a step
+  int left;        // positions of the range behind this piece
+  int done;        // steps up to its end
   int chunks;      // CTAs that take a chunk
   // Softmax warps: phases of their piece-wise barriers used so far.
   uint32_t od0, od1, xp;
@@ -522,44 +547,49 @@ struct Walk {
     const Span sp = span_of(p, s, pair);
     lo = sp.lo;
     n = sp.n;
-    first = w > 0 && n >= w ? n - static_cast<int>(static_cast<unsigned>(n) % static_cast<unsigned>(w)) : 0;
+    g = step_cost(p, s.T, pair);
+    wc = chunk_steps(w, g);
+    first = w > 0 ? chunks_of(n, wc, true) * wc : 0;
   }
-  // False: the range ends within what the item's beginning costs.
-  __device__ __forceinline__ bool piece(int from, int cost) {
-    left -= cost;
-    if (left <= 0) return false;
-    i0 = from;
-    i1 = min(n, i0 + left);
-    left -= i1 - i0;
+  // The item's rest from its position r on: true if a step begins in the range.
+  __device__ __forceinline__ bool piece(int r) {
+    const int all = rest_cost(n - first, g), end = min(all, r + left);
+    left -= all - r;
+    i0 = first + (max(r - kItemCost, 0) + g - 1) / g;
+    i1 = first + (max(end - kItemCost, 0) + g - 1) / g;
+    if (i1 <= i0) return false;
     rot = i0 == first && i1 == n ? done % (n - first) : 0;
     done += i1 - i0;
     return true;
   }
   __device__ __forceinline__ void start(const Params& p, const Head& h, const Start& st, int c) {
-    b = st.b, g = st.g, pair = st.pair, chunk = st.chunk;
-    w = h.chunks > 0 ? static_cast<int>(h.w) : 0;
-    const long long rest = h.rest - (c - h.chunks) * h.w;
-    left = static_cast<int>(c < h.chunks || rest > h.w ? h.w : rest);
+    b = st.b, head = st.g, pair = st.pair, chunk = st.chunk;
+    chunks = h.chunks;
+    w = h.chunks > 0 ? h.w : 0;
     done = 0;
     od0 = od1 = xp = 0;
-    chunks = h.chunks;
     more = 1;
     s = load_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
     item(p);
-    // (a range may begin within the positions before an item's first step)
-    const bool rests = c >= h.chunks;
-    const long long into = (c - h.chunks) * h.w - st.rest;
-    more = piece(st.i, rests && into < kItemCost ? static_cast<int>(kItemCost - into) : 0) ? 1 : 0;
+    if (c < h.chunks) {
+      i0 = st.i;
+      i1 = i0 + wc;
+      rot = left = 0;
+      return;
+    }
+    const long long at = static_cast<long long>(c - h.chunks) * h.w, behind = h.rest - at;
+    left = behind < h.w ? static_cast<int>(behind) : h.w;
+    if (!piece(static_cast<int>(at - st.rest))) next(p);
   }
   __device__ __forceinline__ void next(const Params& p) {
-    more = 0;
-    if (left <= 0) return;
-    do {  // (an item may be all chunks)
-      if (w > 0) chunk += first / w;
+    do {
+      more = 0;
+      if (left <= 0) return;
+      if (w > 0) chunk += first / wc;
       if (++pair >= pairs_of(p, s.T)) {
         pair = 0;
-        if (++g >= p.Hkv) {
-          g = 0;
+        if (++head >= p.Hkv) {
+          head = 0;
           do {
             if (++b >= p.B) return;  // (the plan's range ends before this)
             s = load_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());
@@ -567,8 +597,8 @@ struct Walk {
         }
       }
       item(p);
-    } while (first == n);
-    more = piece(first, kItemCost) ? 1 : 0;
+      more = 1;
+    } while (!piece(0));
   }
   __device__ __forceinline__ int steps() const { return i1 - i0; }
   __device__ __forceinline__ bool whole() const { return i0 == 0 && i1 == n; }
@@ -582,7 +612,7 @@ struct Walk {
     return pair * NQT * p.tt + p.tt < s.T;
   }
 };
-static_assert(sizeof(Walk) <= 96, "shared memory of a warp's walk");
+static_assert(sizeof(Walk) <= 104, "shared memory of a warp's walk");
 
 // The warp's walk to its next piece; false at the end of the range.
 __device__ __forceinline__ bool walk_on(Walk& w, const Params& p, int lane) {
@@ -668,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   grid_wait();  // the plan's writes (and the caller's before it) are visible
   grid_launch_dependents();
-  Walk& w = *reinterpret_cast<Walk*>(smem + C::kWalkOff + warp * 96);
+  Walk& w = *reinterpret_cast<Walk*>(smem + C::kWalkOff + warp * 104);
   bool work;
   Head h;
   Start st;
@@ -677,6 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (work) {
       if (lane == 0) w.start(p, h, st, c);
       __syncwarp();
+      work = w.more != 0;  // (a short last range may hold no step's beginning)
       if (threadIdx.x == 0) p.plan.starts[c] = st;  // for the gather, as is the head
     }
     if (c == 0 && warp == 0) {
@@ -692,6 +723,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (work) {
       st = plan_find(p, h, rest_at, chunk_at, c, lane);  // (every warp for itself)
       if (lane == 0) w.start(p, h, st, c);
+      __syncwarp();
+      work = w.more != 0;
       if (threadIdx.x == 0) p.plan.starts[c] = st;  // for the gather, as is the head
     }
     if (c == 0 && threadIdx.x == 0) *p.plan.head = h;
@@ -699,8 +732,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     h = *p.plan.head;
     work = c < h.ctas;
-    if (work && lane == 0) w.start(p, h, p.plan.starts[c], c);
-    __syncwarp();
+    if (work) {
+      if (lane == 0) w.start(p, h, p.plan.starts[c], c);
+      __syncwarp();
+      work = w.more != 0;
+    }
   }
 
   if (!work) {
@@ -728,14 +764,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&q_full[t], q_bytes);
           for (int x = 0; x < C::kBoxes; ++x)
             tma_load_4d(sQ + t * C::kTileBytes + x * C::kBoxBytes, &tm_q, &q_full[t], x * 64, 0,
-                        w.g, w.s.q0 + (w.pair * NQT + t) * p.tt);
+                        w.head, w.s.q0 + (w.pair * NQT + t) * p.tt);
         }
         ++qn[t];
       }
       // The page that this lane loads of key tile j: its id, or num_pages
       // (out of range: zeros) where the sequence has none.
       const int* row = p.table + static_cast<size_t>(w.b) * p.width;
-      const int keys = w.s.L, g = w.g, n = w.steps();
+      const int keys = w.s.L, g = w.head, n = w.steps();
       const int j0 = w.lo + w.i0;
       int at = w.rot;  // step of the piece
       auto page_of = [&](int j) {
@@ -1135,7 +1171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (w.whole()) {
           // Each thread writes its own row, a 32-byte sector at a time. (Through
           // shared memory, in whole lines, it took twice as long.)
-          const size_t orow = (static_cast<size_t>(w.s.q0) + tok) * p.Hq + w.g * p.G + r % p.G;
+          const size_t orow = (static_cast<size_t>(w.s.q0) + tok) * p.Hq + w.head * p.G + r % p.G;
           T* dst = reinterpret_cast<T*>(p.o) + orow * p.d;
           const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
 #pragma unroll
@@ -1215,19 +1251,18 @@ __global__ void __launch_bounds__(256) attn_paged_gather_kernel(const Params p) 
   const int tile = blockIdx.y / 4, t0 = (nx.pair * NQT + tile) * p.tt;
   const int r0 = (blockIdx.y & 3) * 32;  // rows r0 .. r0 + 31 of the tile
   if (r0 >= p.tt * p.G || t0 + r0 / p.G >= s.T) return;  // none
-  const int n = span_of(p, s, nx.pair).n;
-  const int f = chunks_of(n, h.w, h.chunks > 0);
-  const int rest = static_cast<int>(n - f * h.w);
-  if (has_chunks) {
-    if (nx.i != 0 || (f == 1 && rest == 0)) return;  // not the first chunk, or the whole item
-  } else if (f > 0 || nx.i == 0) {
-    return;  // chunks' business, or a boundary between items
-  }
-  // Its partials: chunks c .. c + f - 1, then the CTAs q0 .. q1 of the rest.
-  const int q0 = h.chunks + static_cast<int>(div_pos(nx.rest + kItemCost, h.w));
-  const int q1 = rest > 0 ? h.chunks + static_cast<int>(div_pos(nx.rest + kItemCost + rest - 1, h.w))
-                          : q0 - 1;
-  if (!has_chunks && q0 != c) return;  // begun before c
+  const int n = span_of(p, s, nx.pair).n, g = step_cost(p, s.T, nx.pair);
+  const int wc = chunk_steps(h.w, g), f = chunks_of(n, wc, h.chunks > 0), rest = n - f * wc;
+  if (has_chunks ? nx.i != 0 || (f == 1 && rest == 0) : f > 0)
+    return;  // not the first chunk, or the whole item; the chunks' business
+  // Its partials: chunks c .. c + f - 1, then the CTAs q0 .. q1 of the rest
+  // (in whose ranges its first and its last step begin).
+  const long long at = nx.rest + kItemCost;
+  const int q0 = h.chunks + static_cast<int>(div_pos(at, h.w));
+  const int q1 =
+      rest > 0 ? h.chunks + static_cast<int>(div_pos(at + static_cast<long long>(rest - 1) * g, h.w))
+               : q0 - 1;
+  if (!has_chunks && (q0 != c || q1 == q0)) return;  // not begun in c's range, or not cut
   const int parts = f + q1 - q0 + 1;
   auto slot_of = [&](int k) {
     if (k < f) return c + k;
