@@ -474,14 +474,15 @@ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 struct PsLayout {
   size_t tok_off, tile_off, starts, part_o, part_lse, total;
 };
-inline PsLayout ps_layout(int B, int Hkv, int G, int d, int nc, bool partials) {
+inline PsLayout ps_layout(int B, int Hkv, int G, int d, int nc, bool partials,
+                          size_t slots = 0) {  // 0: a slot for each (segment + cta)
   PsLayout L;
   L.tok_off = 0;
   L.tile_off = align_up(static_cast<size_t>(B) * 8, 256);
   size_t end = L.tile_off + (static_cast<size_t>(B) + 1) * 4;
   L.starts = L.part_o = L.part_lse = 0;
   if (partials) {
-    const size_t slots = static_cast<size_t>(B) * Hkv + nc - 1;
+    if (slots == 0) slots = static_cast<size_t>(B) * Hkv + nc - 1;
     L.starts = align_up(end, 256);
     end = L.starts + static_cast<size_t>(nc) * 16;
     L.part_o = align_up(end, 256);

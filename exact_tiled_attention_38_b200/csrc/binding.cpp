@@ -184,7 +184,18 @@ struct Place {
       stream = reinterpret_cast<attn_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream());
     else
       stream = reinterpret_cast<attn_stream_t>(PyLong_AsUnsignedLongLong(s));
+    given = s != Py_None;
+    device = static_cast<c10::DeviceIndex>(dev);
   }
+  // A tensor allocated here (on the current stream) for work on another one:
+  // its memory is not handed out again before that work is done.
+  void allocated(const at::Tensor& t) const {
+    if (given && t.defined())
+      t.record_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream), device)
+                          .unwrap());
+  }
+  bool given;
+  c10::DeviceIndex device;
 };
 
 template <typename F, typename... A>
@@ -215,6 +226,9 @@ struct Out {
   at::Tensor t;
   PyObject* given;  // borrowed, or NULL
   PyObject* result() const { return given ? again(given) : wrap(t); }
+  void keep(const Place& place) const {
+    if (!given) place.allocated(t);
+  }
 };
 
 Out int32_out(PyObject* o, const char* name, const at::Tensor& like, int dev, at::IntArrayRef sizes) {
@@ -259,6 +273,8 @@ PyObject* paged(PyObject* const* a) {
   const int code = call(lib.paged[c.type], q.data_ptr(), stride, &c.c, cu, lens, o.t.data_ptr(), lse_p,
                         c.B, Hq, total, max_q, scale, window, place.stream);
   if (code != ATTN_OK) return PyLong_FromLong(code);
+  o.keep(place);
+  lse.keep(place);
   return give({o.result(), lse.t.defined() ? lse.result() : again(Py_None)});
 }
 
@@ -321,6 +337,8 @@ PyObject* rope(PyObject* const* a) {
            k ? static_cast<int>(k->size(1)) : 0, static_cast<int>(N), static_cast<int>(d), rot, amp,
            truth(a[5]) ? 1 : 0, truth(a[8]) ? 1 : 0, place.stream);
   if (code != ATTN_OK) return PyLong_FromLong(code);
+  qo.keep(place);
+  ko.keep(place);
   return give({qo.result(), k ? ko.result() : again(Py_None)});
 }
 
@@ -353,6 +371,7 @@ PyObject* append(PyObject* const* a) {
                         v.data_ptr(), vs, &c.c, cu, lens, pos, turns.data_ptr<double>(), c.B, Hq,
                         total, rot, amp, truth(a[10]) ? 1 : 0, place.stream);
   if (code != ATTN_OK) return PyLong_FromLong(code);
+  o.keep(place);
   return o.result();
 }
 
@@ -373,6 +392,7 @@ PyObject* update(PyObject* const* a) {
                         source, add, t.t.data_ptr<int32_t>(), l.t.data_ptr<int32_t>(),
                         r.t.data_ptr<int32_t>(), info.t.data_ptr<int32_t>(), c.B, place.stream);
   if (code != ATTN_OK) return PyLong_FromLong(code);
+  for (const Out* x : {&t, &l, &r, &info}) x->keep(place);
   return give({t.result(), l.result(), r.result(), info.result()});
 }
 
@@ -390,6 +410,7 @@ PyObject* compact(PyObject* const* a) {
                         t.t.data_ptr<int32_t>(), r.t.data_ptr<int32_t>(),
                         info.t.data_ptr<int32_t>(), c.B, place.stream);
   if (code != ATTN_OK) return PyLong_FromLong(code);
+  for (const Out* x : {&t, &r, &info}) x->keep(place);
   return give({t.result(), r.result(), info.result()});
 }
 

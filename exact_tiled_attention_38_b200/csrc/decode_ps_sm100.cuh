@@ -1192,11 +1192,13 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
     bool ok = true;
     uint32_t xc = 0;        // uses of the x_bar / red exchange so far
     bool piece_whole = false;
+    [[maybe_unused]] bool piece_begins = false;  // the piece begins its segment
     for (int j = 0; j < n; ++j) {
       const bool first = (j == 0) || (cur.i == 0);
       const bool last = (j == n - 1) || (cur.i == cur.nt - 1);
       if (first) {
         piece_whole = (cur.i == 0);
+        piece_begins = piece_whole;
 #pragma unroll
         for (int h = 0; h < GPT; ++h) {
           m[h] = -INFINITY;
@@ -1362,7 +1364,8 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
                 if (dim == hg && p.lse != nullptr) p.lse[row0 + hg] = l2 * 0.69314718055994531f;
               }
             } else {
-              const size_t slot = static_cast<size_t>(seg) + c;
+              const size_t slot = PAGED ? static_cast<size_t>(2 * c + (piece_begins ? 1 : 0))
+                                        : static_cast<size_t>(seg) + c;
               const int R = PAGED ? p.R : G;
               p.part_o[(slot * R + hg) * D + dim] = ov;
               if (dim == (PAGED ? 0 : hg)) p.part_lse[slot * R + hg] = l2;
@@ -1425,6 +1428,9 @@ __global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p
   const int c1 = cta_of(a + nt - 1, T_all, nc);
   if (c0 == c1) return;
   const long long seg = static_cast<long long>(b) * p.Hkv + g;
+  auto slot_of = [&](int cc) -> long long {
+    return PAGED ? 2 * cc + (cc == c0 ? 1 : 0) : seg + cc;
+  };
   // CTAs between c0 and c1 with an empty tile range (possible only with
   // fewer tiles than CTAs) wrote nothing: their slots are skipped. The
   // partials of the first kMaxP CTAs are all loaded before any is used, so
@@ -1441,7 +1447,7 @@ __global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p
     const int cc = c0 + k;
     lse_r[k] = -INFINITY;
     if (cc <= c1 && has_tiles(cc)) {
-      const long long slot = (seg + cc) * R + hh;
+      const long long slot = slot_of(cc) * R + hh;
       lse_r[k] = p.part_lse[slot];
       const float* x = p.part_o + slot * D + lane * EPL;
       if constexpr (EPL == 4) {
@@ -1472,7 +1478,7 @@ __global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p
   for (int k = 0; k < kMaxP; ++k) fold(lse_r[k], xv[k]);
   for (int cc = c0 + kMaxP; cc <= c1; ++cc) {
     if (!has_tiles(cc)) continue;
-    const long long slot = (seg + cc) * R + hh;
+    const long long slot = slot_of(cc) * R + hh;
     const float* x = p.part_o + slot * D + lane * EPL;
     float xr[EPL];
 #pragma unroll

@@ -193,7 +193,9 @@ int paged_decode_run(const void* q, long long q_stride, const paged::Cache& c, c
   int rc = encode_queries(&tq, q, q_stride, c, G, total_q, max_q, bf16);
   if (rc == ATTN_OK) rc = encode_pools(&kv.k, &kv.v, c, bf16);
   if (rc != ATTN_OK) return rc;
-  const PsLayout L = ps_layout(B, c.Hkv, p.R, D, nc, true);
+  // Two slots of partial rows a CTA: what goes on from the CTA before, and what
+  // goes on in the next.
+  const PsLayout L = ps_layout(B, c.Hkv, p.R, D, nc, true, 2 * static_cast<size_t>(nc));
   Workspace ws;
   rc = ws.take(L.total, st);
   if (rc != ATTN_OK) return rc;
@@ -270,11 +272,11 @@ int paged_run(const void* q, long long q_stride, const attn_pages* pages, const 
 
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   const int tt = paged::BM / G;
-  // (a CTA's steps are counted in 32 bits: with the longest cache that the
-  // table allows for every token, this is years of work)
+  // (a CTA's steps are counted in 32 bits, each as up to 9 positions: with the
+  // longest cache that the table allows for every token, this is weeks of work)
   const double most_steps = (static_cast<double>(total_q) / (paged::NQT * tt) + B) * c.Hkv *
                             (static_cast<double>(c.capacity()) / paged::BN + 1);
-  if (most_steps / info.sm_count > 2e9) return ATTN_ERR_UNSUPPORTED;
+  if (most_steps / info.sm_count > 2e8) return ATTN_ERR_UNSUPPORTED;
   CUtensorMap tq, tk, tv;
   int rc = encode_queries(&tq, q, q_stride, c, G, total_q, tt, bf16);
   if (rc == ATTN_OK) rc = encode_pools(&tk, &tv, c, bf16);
@@ -300,7 +302,7 @@ int paged_run(const void* q, long long q_stride, const attn_pages* pages, const 
   p.window = window;
   p.nc = info.sm_count;
   p.inline_plan = B <= paged::kInlineB ? 1 : 0;
-  p.warp_plan = B <= 32 && most_steps < 1e9 ? 1 : 0;
+  p.warp_plan = B <= 32 && most_steps < 2e8 ? 1 : 0;
   p.max_pairs = (max_q + paged::NQT * tt - 1) / (paged::NQT * tt);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_ns = kDefaultWaitNs;

@@ -316,9 +316,12 @@ typedef struct attn_pages {
  * d <= 128 with at most 128 query heads per KV head runs on the tensor cores
  * (any d below 64 or 128 at the cost of that size), other sizes on a CUDA-core
  * kernel, far from the former's speed.
- * Device memory: one workspace block from the library's pool, as attn_decode:
- * on the tensor cores (B + 1) * 8 bytes, and per SM 16 bytes and
- * 2 * 256 * (d + 1) * 4 bytes of partial results; else none.
+ * Device memory: one workspace block from the library's pool, as attn_decode.
+ * With D = 64 or 128, the least that holds d: max_q * Hq / Hkv <= 32 rows (16
+ * for several tokens at d <= 64) take 12 bytes per sequence and per SM
+ * 2 * max_q * (Hq / Hkv) * (D + 1) * 4 bytes of partial results; more rows take
+ * 3 * 256 * (D + 1) * 4 bytes per SM, and 12 bytes per sequence above 2048 of
+ * them; a few hundred bytes come on top. The CUDA-core kernel takes none.
  */
 int attn_paged(const void* q, long long q_stride, const attn_pages* cache, const int32_t* cu_q,
                const int32_t* kv_lens, void* o, float* lse, int B, int Hq, int total_q, int max_q,
@@ -425,8 +428,9 @@ int attn_rope_turns(double* turns, float* amp, int rot, double base, int scaling
  * All DEVICE memory. Values have 2 bytes; a page's Hkv * page_size * d values
  * must lie in one piece (either order); layer l of the pools begins
  * l * layer_stride elements behind k and v. Whole-number results do not depend
- * on timing. One workspace block of (2 B + 3 max(B, num_pages)) * 4 bytes and a
- * little more, as in attn_decode.
+ * on timing. Caches of more than some 25,000 pages, or tables of more than
+ * 65,536 entries in all, take one workspace block of (2 B + 3 max(B, num_pages))
+ * * 4 bytes and a little more, as in attn_decode; smaller ones none.
  */
 int attn_pages_update(const attn_pages* cache, int layers, long long layer_stride,
                       const int32_t* lens, const int32_t* refs, const int32_t* source,

@@ -53,6 +53,8 @@ CASES = {
     "chunk_group_7_d64": ("f16", 64, 14, 2, 32, [65, 3, 130], [900, 300, 131], 0),
     "chunk_over_long": ("bf16", 128, 8, 2, 128, [100], [3001], 0),
     "chunk_page_256": ("f16", 128, 8, 8, 256, [129, 1], [700, 513], 0),
+    "chunk_page_512": ("bf16", 64, 4, 2, 512, [40, 1], [700, 1025], 0),
+    "decode_page_1024": ("f16", 128, 8, 2, 1024, [1, 1], [1030, 5], 700),
     "chunk_page_8": ("bf16", 64, 8, 2, 8, [40, 200], [333, 200], 0),
     "chunk_window": ("bf16", 128, 8, 2, 16, [200, 64, 1], [1000, 64, 700], 130),
     "window_of_one": ("f16", 64, 8, 2, 16, [70, 1], [400, 129], 1),
@@ -236,6 +238,24 @@ def test_agrees_with_contiguous_prefill_and_packed_decode(lib):
                              torch.tensor([N], dtype=torch.int32).cuda(), Hkv=2)
     assert (o1.float() - od.float()).abs().max() <= 2.0 ** -7 * od.float().abs().max()
     assert (l1 - ld).abs().max() < 1e-4
+
+
+def test_outputs_on_a_given_stream_keep_their_memory(lib):
+    """Outputs that the call allocates for another stream are not handed out again, once
+    dropped, before that stream is done with them."""
+    T, L = [200], [30000]
+    kp, vp, table, _ = make_cache(L, 2, 64, 64, torch.bfloat16, 51)
+    q = randn((200, 8, 64), torch.bfloat16, 52)
+    st = [x.cuda() for x in (q, kp, vp, table, cu(T), torch.tensor(L, dtype=torch.int32))]
+    want, _ = lib.attn_paged(*st)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    keep = []
+    for _ in range(30):
+        lib.attn_paged(*st, stream=side)  # dropped at once
+        keep.append(torch.zeros_like(want))  # would take its place, on the current stream
+    torch.cuda.synchronize()
+    assert not any(t.any() for t in keep)
 
 
 def plain(q, kp, vp, table, T, L, scale, window, rows):

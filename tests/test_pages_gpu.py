@@ -53,7 +53,7 @@ def test_update(lib, name, layers):
     check_update(lib, kp, vp, table, lens, refs, source, add, 16, "tokens_outermost")
 
 
-@pytest.mark.parametrize("B,page,seed", [(1, 8, 1), (7, 8, 2), (33, 64, 3), (100, 16, 4), (1500, 8, 5)])
+@pytest.mark.parametrize("B,page,seed", [(1, 8, 1), (7, 8, 2), (33, 64, 3), (100, 16, 4), (1500, 8, 5), (1700, 64, 6)])
 def test_update_random_steps(lib, B, page, seed):
     """Several steps one after another: shared pages, forks of forks, ends and starts."""
     rng = np.random.default_rng(seed)
@@ -95,7 +95,8 @@ def test_update_pinned_pages_and_bad_sources(lib):
 @pytest.mark.parametrize("layers", [None, 2])
 @pytest.mark.parametrize("lens,page,spare,seed", [
     ([5, 16, 0, 31], 8, 0, 1), ([5, 16, 0, 31], 8, 1, 2), ([5, 16, 0, 31], 8, 50, 3), ([], 8, 9, 4),
-    ([0, 0], 16, 5, 5), ([300] * 20, 16, 9000, 6), ([1] * 900, 8, 20000, 7), ([700, 20], 64, 3, 8)])
+    ([0, 0], 16, 5, 5), ([300] * 20, 16, 9000, 6), ([1] * 900, 8, 20000, 7), ([700, 20], 64, 3, 8),
+    ([9] * 700, 8, 30000, 9), ([40] * 1000, 8, 10, 10)])
 def test_compact(lib, lens, page, spare, seed, layers):
     kp, vp, table, refs = make_cache(lens, 1, 8, page, torch.float16, seed, spare=spare, layers=layers)
     if len(lens) > 2:  # two rows that share a page
@@ -131,6 +132,37 @@ def test_large_pages_and_layer_views(lib):
     for a, b in copies:
         kp[:, b], vp[:, b] = kp[:, a], vp[:, a]
     assert torch.equal(kg.cpu(), kp) and torch.equal(vg.cpu(), vp)
+
+
+def test_offsets_beyond_32_bits(lib):
+    """Pages more than 2^31 values apart (one layer of a pool with all layers side by side):
+    append, attention of one token and of a chunk, update and compaction."""
+    lens, page, Hkv, d, Hq = [40, 100], 16, 2, 64, 4
+    kp, vp, table, refs = make_cache(lens, Hkv, d, page, torch.bfloat16, 8, spare=6, width=9)
+    P, n = kp.shape[0], Hkv * page * d
+    wide = (1 << 32) // (P - 2) // 8 * 8  # values between pages: the last ones lie behind 2^32
+    big = torch.empty((P - 1) * wide + 2 * n, dtype=torch.bfloat16, device="cuda")
+    view = lambda at: big.as_strided((P, Hkv, page, d), (wide, page * d, d, 1), at)  # noqa: E731
+    kg, vg = view(0), view(n)
+    kg.copy_(kp)
+    vg.copy_(vp)
+    kd, vd = kp.cuda(), vp.cuda()
+    turns = lib.attn_rope_turns(64)[0].cuda()
+    for T in ([1, 1], [30, 90]):
+        x = randn((sum(T), Hq + 2 * Hkv, d), torch.bfloat16, 9).cuda()
+        got = []
+        for k, v in ((kg, vg), (kd, vd)):
+            q = lib.attn_rope_append(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], k, v, table.cuda(), cu(T).cuda(),
+                                     ints(lens), turns)
+            got.append((q, *lib.attn_paged(q, k, v, table.cuda(), cu(T).cuda(), ints(lens), max_q=max(T))))
+        assert all(torch.equal(a, b) for a, b in zip(*got))
+        assert torch.equal(kg, kd) and torch.equal(vg, vd)
+    for k, v in ((kg, vg), (kd, vd)):
+        out = lib.attn_pages_update(k, v, table.cuda(), ints(lens), refs.cuda(), ints([1, 1]), ints([1, 20]))
+        got.append(out + lib.attn_pages_compact(k, v, out[0], out[1], out[2]))
+    assert all(torch.equal(a, b) for a, b in zip(got[2], got[3]))
+    assert torch.equal(kg, kd) and torch.equal(vg, vd) and int(got[2][6][1]) >= 0
+    assert lib.attn_get_device_status()[0] == lib.ATTN_OK
 
 
 def test_capture_two_graphs_and_streams(lib):
