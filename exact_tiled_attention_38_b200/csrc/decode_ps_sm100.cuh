@@ -49,6 +49,17 @@
 // 128-byte-swizzled layout, zero-filled past the segment's last key (the
 // packed cache's extent is only known on the device).
 //
+// Over a paged cache (PAGED; attn_paged with few rows of a KV head) the same
+// pass takes the rows of all new tokens of a sequence, up to 32, where it has
+// heads; K and V come by TMA, a lane per page and 64 columns, into the tiles
+// that begin where the cache's do (16-byte copies whose addresses went through
+// the page table kept the ring waiting: 283 us on the ragged batch below, 195
+// us by TMA, 0.95 of the measured copy rate); rows of V behind a sequence's
+// last key are set to zero before the product; a cut segment's partials go to
+// two slots a CTA. 4 sequences of 30-700 tokens, 32/8 heads: 9.8 us, of which
+// 6 us are the chain start, plan, page id, K, scores, V, output, and 3 us the
+// gather's.
+//
 // Warp roles (HS softmax warps per key quarter): warps 0 .. 4 HS - 1 softmax
 // and epilogue, then the tensor memory owner (MMA issue and Q loads, whole
 // warp, one elected lane), then three producers, each owning one ring stage.

@@ -54,6 +54,15 @@
 // O; group 0 folds O_1 into O_0 at the end of the piece. One group's
 // exponentials then overlap the other's products and loads.
 //
+// Bound by the tensor cores and the exponential unit together, like the
+// prefill kernel (a pair's step of 2 x 128 x 128 scores takes 3,500 cycles at d
+// = 128 where either needs 2,048; 3,000 at d = 64), and at its ends by the
+// chain of loads of a start (about 4 us) and the gather (4 us). Measured on
+// B200: 1024 tokens over 64K, 32/8 heads, d = 128 0.87-0.89 ms once, 1.02-1.03
+// ms in a row under the power limit (1.06 PFLOP/s, 0.76 of the measured
+// sustained rate); 9 sequences of up to 301 tokens under a window of 4096, 16/2
+// heads, d = 64 54 us.
+//
 // Rows of V behind the sequence's last key are set to zero in shared memory
 // before the product: their probabilities are zero, but what lies there in the
 // pool may be infinite or NaN.

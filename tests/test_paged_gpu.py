@@ -32,7 +32,7 @@ def check(lib, o, lse, q, kp, vp, table, c, L, scale, window=0):
     bad = rows & ~empty
     over = (np.abs(o - ro) / bo)[bad]
     assert over.max(initial=0) <= 1, f"o is {over.max():.2f} bounds off"
-    over = (np.abs(lse - rl) / (bl + 2.0 ** -23 * np.abs(rl)))[bad]
+    over = np.abs(lse[bad] - rl[bad]) / (bl[bad] + 2.0 ** -23 * np.abs(rl[bad]))
     assert over.max(initial=0) <= 1, f"lse is {over.max():.2f} bounds off"
     assert lib.attn_get_device_status()[0] == lib.ATTN_OK
 
