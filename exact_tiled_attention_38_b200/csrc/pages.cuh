@@ -410,16 +410,18 @@ inline size_t update_small_words(int B, int P) {
 inline size_t compact_small_words(int P) { return 2 * static_cast<size_t>(P); }
 
 // Calls f(i, rank) for the entries i of [0, n) where pick(i) holds, rank being
-// their number in order; returns how many there are. A warp takes a contiguous
-// share, 32 entries at a time. `red` holds 33 words.
+// their number in order, as long as it is below `most`; returns how many there
+// are in all. A warp takes a contiguous share, 32 entries at a time. `red`
+// holds 33 words.
 template <typename Pick, typename F>
-__device__ __forceinline__ int each_in_order(int n, int* red, Pick pick, F f) {
+__device__ __forceinline__ int each_in_order(int n, int* red, int most, Pick pick, F f) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int share = (n + kThreads - 1) / kThreads * 32;
   const int i0 = min(n, warp * share), i1 = min(n, i0 + share);
   int mine = 0;
-  for (int i = i0 + lane; i - lane < i1; i += 32)
-    mine += __popc(__ballot_sync(0xffffffffu, i < i1 && pick(i)));
+#pragma unroll 4
+  for (int i = i0 + lane; i < i1; i += 32) mine += pick(i) ? 1 : 0;
+  mine = __reduce_add_sync(0xffffffffu, mine);
   __syncthreads();  // red's last use
   if (lane == 0) red[warp] = mine;
   __syncthreads();
@@ -432,10 +434,11 @@ __device__ __forceinline__ int each_in_order(int n, int* red, Pick pick, F f) {
   }
   int at = __shfl_sync(0xffffffffu, x - v, warp);
   const int all = __shfl_sync(0xffffffffu, x, 31);
-  for (int i = i0 + lane; i - lane < i1; i += 32) {
+  for (int i = i0 + lane; i - lane < i1 && at < most; i += 32) {
     const bool p = i < i1 && pick(i);
     const unsigned m = __ballot_sync(0xffffffffu, p);
-    if (p) f(i, at + __popc(m & ((1u << lane) - 1)));
+    const int k = at + __popc(m & ((1u << lane) - 1));
+    if (p && k < most) f(i, k);
     at += __popc(m);
   }
   return all;
@@ -524,35 +527,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const int n_free = each_in_order(
-      p.P, red, [&](int i) { return refs[i] <= 0; },
-      [&](int i, int k) {
-        if (k < need) list[k] = i;
-      });
+      p.P, red, need, [&](int i) { return refs[i] <= 0; }, [&](int i, int k) { list[k] = i; });
   const bool refused = need > n_free || s_long > 0;
   __syncthreads();
 
-  // The tables, a share of the rows.
-  for (int b = me; b < p.B; b += warps) {
-    int* out = p.table_out + static_cast<size_t>(b) * p.width;
+  // The tables, 32 entries of a row a warp at a time over the whole grid.
+  const int blocks = (p.width + 31) / 32;
+  for (int u = me; u < p.B * blocks; u += warps) {
+    const int b = u / blocks, j = (u - b * blocks) * 32 + lane;
+    const size_t row = static_cast<size_t>(b) * p.width;
+    if (j == 0) p.lens_out[b] = refused ? p.lens[b] : longer[b];
+    if (j >= p.width) continue;
+    int page = -1;
     if (refused) {  // everything stays as it was
-      const int* in = p.table + static_cast<size_t>(b) * p.width;
-      for (int j = lane; j < p.width; j += 32) out[j] = in[j];
-      if (lane == 0) p.lens_out[b] = p.lens[b];
-      continue;
+      page = p.table[row + j];
+    } else if (j < kept[b]) {
+      page = p.table[static_cast<size_t>(max(src[b], 0)) * p.width + j];
+      if (page < 0 || page >= p.P) paged::bad(paged::kBadPage);
+    } else if (j < ceil_pages(longer[b], p.page_log2)) {
+      page = list[first[b] + j - kept[b]];
     }
-    const int k = kept[b], want = ceil_pages(longer[b], p.page_log2), f = first[b];
-    const int* in = p.table + static_cast<size_t>(max(src[b], 0)) * p.width;
-    for (int j = lane; j < p.width; j += 32) {
-      int page = -1;
-      if (j < k) {
-        page = in[j];
-        if (page < 0 || page >= p.P) paged::bad(paged::kBadPage);
-      } else if (j < want) {
-        page = list[f + j - k];
-      }
-      out[j] = page;
-    }
-    if (lane == 0) p.lens_out[b] = longer[b];
+    p.table_out[row + j] = page;
   }
   if (refused) {
     for (int i = blockIdx.x * kThreads + tid; i < p.P; i += gridDim.x * kThreads)
@@ -567,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (refused) return;
   // The copies, in the order of the rows.
   const int copies = each_in_order(
-      p.B, red,
+      p.B, red, p.B,
       [&](int b) { return src[b] >= 0 && ceil_pages(len[src[b]], p.page_log2) > kept[b]; },
       [&](int b, int k) {
         const int of = p.table[static_cast<size_t>(src[b]) * p.width + kept[b]], page = list[first[b]];
@@ -603,10 +598,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The k-th live page from n on takes the k-th hole below n; there are as many
   // of both, so not more than P / 2.
   const int moves = each_in_order(
-      n, red, [&](int i) { return refs[i] <= 0; }, [&](int i, int k) { to[k] = i; });
+      n, red, p.P, [&](int i) { return refs[i] <= 0; }, [&](int i, int k) { to[k] = i; });
   __syncthreads();
   each_in_order(
-      p.P - n, red, [&](int i) { return refs[n + i] > 0; },
+      p.P - n, red, p.P, [&](int i) { return refs[n + i] > 0; },
       [&](int i, int k) {
         from[k] = n + i;
         refs[to[k]] = refs[n + i];
@@ -615,21 +610,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   for (int i = blockIdx.x * kThreads + tid; i < p.P; i += gridDim.x * kThreads)
     p.refs_out[i] = i < n ? refs[i] : 0;
-  for (int b = me; b < p.B; b += warps) {
-    const int l = p.lens[b], L = clamp_len(l, p), held = ceil_pages(L, p.page_log2);
-    if (lane == 0 && l > L) paged::bad(paged::kBadLength);
-    for (int j = lane; j < p.width; j += 32) {
-      const size_t e = static_cast<size_t>(b) * p.width + j;
-      int page = -1;
-      if (j < held) {
-        page = p.table[e];
-        if (page < 0 || page >= p.P || p.refs[page] <= 0)
-          paged::bad(paged::kBadPage);  // (left as it was)
-        else if (page >= n)
-          page = ~refs[page];
-      }
-      p.table_out[e] = page;
+  const int blocks = (p.width + 31) / 32;
+  for (int u = me; u < p.B * blocks; u += warps) {
+    const int b = u / blocks, j = (u - b * blocks) * 32 + lane;
+    const int l = p.lens[b], L = clamp_len(l, p);
+    if (j == 0 && l > L) paged::bad(paged::kBadLength);
+    if (j >= p.width) continue;
+    const size_t e = static_cast<size_t>(b) * p.width + j;
+    int page = -1;
+    if (j < ceil_pages(L, p.page_log2)) {
+      page = p.table[e];
+      if (page < 0 || page >= p.P || p.refs[page] <= 0)
+        paged::bad(paged::kBadPage);  // (left as it was)
+      else if (page >= n)
+        page = ~refs[page];
     }
+    p.table_out[e] = page;
   }
   if (blockIdx.x == 0 && tid == 0) {
     p.info[0] = n;
