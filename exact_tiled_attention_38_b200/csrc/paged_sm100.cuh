@@ -1178,6 +1178,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; ++e) f[e] = 0.f;
           }
         };
+        // (The loops over columns stay loops: this code runs once a piece, and a
+        // small batch runs it on a cold instruction cache.)
         const float l2 = l > 0.f ? m + lg2_approx(l) : -INFINITY;
         if (w.whole()) {
           // Each thread writes its own row, a 32-byte sector at a time. (Through
@@ -1185,7 +1187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const size_t orow = (static_cast<size_t>(w.s.q0) + tok) * p.Hq + w.head * p.G + r % p.G;
           T* dst = reinterpret_cast<T*>(p.o) + orow * p.d;
           const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
-#pragma unroll
+#pragma unroll 1
           for (int col = 0; col < D; col += 32) {
             float f[32];
             columns(col, f);
@@ -1214,7 +1216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const size_t rows32 = static_cast<size_t>(w.slot(c, p.nc)) * (kSlotRows / 32) +
                                 (tile * BM + (warp & 3) * 32) / 32;
           float4* dst = reinterpret_cast<float4*>(p.part_o) + rows32 * (8 * D) + lane;
-#pragma unroll
+#pragma unroll 1
           for (int col = 0; col < D; col += 32) {
             float f[32];
             columns(col, f);
