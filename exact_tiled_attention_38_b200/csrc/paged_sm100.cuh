@@ -1015,6 +1015,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!live) {  // no rows in this warp: its P is never stored
             if constexpr (C::kOwnP) {
               mbar_arrive(&s_free[t]);
+              // In step with the warps that have rows: the next scores come before
+              // this step's product here, so an arrival for the next step could
+              // otherwise stand in for one that this step's P still needs.
+              if (np > 0 &&
+                  !(ok = warp_all(wait_bar(&pv_done[t], (np - 1) & 1, ctl, kSitePvDone))))
+                break;
               ++np;
             }
             mbar_arrive(&p_ready[t]);
@@ -1066,6 +1072,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = m_tile;
             l *= alpha;
           }
+          __syncwarp();  // tensor memory is written by the whole warp together
           const float m_use = (m == -INFINITY) ? 0.f : m;
           if constexpr (C::kOwnP) {
             // The first half of P in registers while the previous product may
@@ -1160,9 +1167,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         w0 *= inv;
         w1 *= inv;
         // 32 columns of the row's O, normalised; zeros for a row without keys
-        // (O may hold anything).
+        // (O may hold anything). The whole warp reads tensor memory together, so
+        // the lanes that have a row and those that have none meet here first.
         auto columns = [&](int col, float (&f)[32]) {
           uint32_t o[32];
+          __syncwarp();
           tmem_ld_x32(tmem + lane_off + C::o_col(t) + col, o);
           tmem_wait_ld_x32(o);
 #pragma unroll
@@ -1191,24 +1200,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int col = 0; col < D; col += 32) {
             float f[32];
             columns(col, f);
-            if (!row_ok) continue;
+            if (row_ok) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint32_t v[8];
+              for (int u = 0; u < 2; ++u) {
+                uint32_t v[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                v[e] = prefill::pack2<T>(f[16 * u + 2 * e], f[16 * u + 2 * e + 1]);
-              const int at = col + 16 * u;
-              if (sectors && at + 16 <= p.d) {
-                st_global_32(dst + at, v);
-              } else {
-                if (at < p.d) *reinterpret_cast<uint4*>(dst + at) = make_uint4(v[0], v[1], v[2], v[3]);
-                if (at + 8 < p.d)
-                  *reinterpret_cast<uint4*>(dst + at + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+                for (int e = 0; e < 8; ++e)
+                  v[e] = prefill::pack2<T>(f[16 * u + 2 * e], f[16 * u + 2 * e + 1]);
+                const int at = col + 16 * u;
+                if (sectors && at + 16 <= p.d) {
+                  st_global_32(dst + at, v);
+                } else {
+                  if (at < p.d)
+                    *reinterpret_cast<uint4*>(dst + at) = make_uint4(v[0], v[1], v[2], v[3]);
+                  if (at + 8 < p.d)
+                    *reinterpret_cast<uint4*>(dst + at + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+                }
               }
             }
           }
           if (row_ok && p.lse != nullptr) p.lse[orow] = l2 * 0.69314718055994531f;
+          __syncwarp();
         } else {
           // A partial, 32 rows of the slot per warp: columns 4u .. 4u + 3 of
           // all rows side by side, so that what a thread holds goes out in

@@ -375,6 +375,37 @@ def test_items_of_two_tiles_and_of_one_in_turns(lib, d):
         again, lse2 = lib.attn_paged(*st, max_q=64)
         assert torch.equal(o, again) and torch.equal(lse, lse2)
 
+@pytest.mark.parametrize("dtype, d, window", [("f16", 64, 0), ("f16", 64, 1024), ("bf16", 128, 0), ("bf16", 96, 300)])
+def test_warps_without_rows_every_time(lib, dtype, d, window):
+    """Row tiles with warps that have no row and warps that have some, first and second tiles of an
+    item, whole items and cut ones, over many key tiles: the oracle's result, and the same bits
+    whatever runs before and however cold the caches are. (A warp without rows once ran a step
+    ahead of its tile's others, whose probabilities the product then missed.)"""
+    dtype = DTYPES[dtype]
+    T = [98, 34, 7, 241, 133, 83, 120, 59, 27]
+    L = [1199, 3010, 917, 4437, 1362, 2307, 4195, 1067, 3552]
+    kp, vp, table, _ = make_cache(L, 2, d, 16, dtype, 17, unused=NAN)
+    q, c = randn((sum(T), 16, d), dtype, 18), cu(T)
+    qd, kd, vd, td, cd = (x.cuda() for x in (q, kp, vp, table, c))
+    ld = torch.tensor(L, dtype=torch.int32, device="cuda")
+
+    def call():
+        return lib.attn_paged(qd, kd, vd, td, cd, ld, max_q=max(T), window=window)
+
+    o, lse = call()
+    check(lib, o, lse, q, kp, vp, table, c, L, d ** -0.5, window)
+    cold = torch.empty(1 << 26, dtype=torch.int32, device="cuda")  # larger than L2
+    outs = []
+    for i in range(60):
+        if i % 3 == 0:
+            cold.fill_(i)
+        elif i % 3 == 1:  # another kernel's code in between
+            cold[: 1 << 16].sort()
+        outs.append(call())
+    for o2, lse2 in outs:
+        assert torch.equal(o2, o) and torch.equal(lse2, lse)
+    assert lib.attn_get_device_status()[0] == lib.ATTN_OK
+
 
 def test_binding_refusals(lib):
     kp, vp, table, _ = make_cache([20], 2, 64, 16, torch.bfloat16, 1)
