@@ -1065,14 +1065,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx3 = fmax3(mx3, s[3 * Q + k], s[3 * Q + k + 1]);
           }
           const float m_tile = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * sl2;
-          float alpha = 1.f;
+          // (Selects, no branch: tensor memory is written by the whole warp together.)
           const bool need = m_tile > m + prefill::kRescaleThreshold;
-          if (need) {
-            alpha = ex2_approx(m - m_tile);  // m = -inf gives 0
-            m = m_tile;
-            l *= alpha;
-          }
-          __syncwarp();  // tensor memory is written by the whole warp together
+          const float alpha = ex2_approx(need ? m - m_tile : 0.f);  // m = -inf gives 0
+          m = need ? m_tile : m;
+          l *= alpha;
           const float m_use = (m == -INFINITY) ? 0.f : m;
           if constexpr (C::kOwnP) {
             // The first half of P in registers while the previous product may
