@@ -58,10 +58,10 @@
 // prefill kernel (a pair's step of 2 x 128 x 128 scores takes 3,500 cycles at d
 // = 128 where either needs 2,048; 3,000 at d = 64), and at its ends by the
 // chain of loads of a start (about 4 us) and the gather (4 us). Measured on
-// B200: 1024 tokens over 64K, 32/8 heads, d = 128 0.87-0.89 ms once, 1.02-1.03
+// B200: 1024 tokens over 64K, 32/8 heads, d = 128 0.88-0.89 ms once, 1.00-1.04
 // ms in a row under the power limit (1.06 PFLOP/s, 0.76 of the measured
 // sustained rate); 9 sequences of up to 301 tokens under a window of 4096, 16/2
-// heads, d = 64 54 us.
+// heads, d = 64 55 us.
 //
 // Rows of V behind the sequence's last key are set to zero in shared memory
 // before the product: their probabilities are zero, but what lies there in the
@@ -1184,8 +1184,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; ++e) f[e] = 0.f;
           }
         };
-        // (The loops over columns stay loops: this code runs once a piece, and a
-        // small batch runs it on a cold instruction cache.)
+        // (The loops over columns stay loops: this code runs once a piece, often on
+        // a cold instruction cache; unrolled, 8K tokens took 497 us where they took
+        // 479.)
         const float l2 = l > 0.f ? m + lg2_approx(l) : -INFINITY;
         if (w.whole()) {
           // Each thread writes its own row, a 32-byte sector at a time. (Through

@@ -22,7 +22,7 @@
 //
 // Bound: the whole numbers by latency (a few dependent passes over the tables
 // and the counts), the contents by memory (each moved page is read once and
-// written once). Measured on B200: a serving step of 64 rows, 8,400 pages 10.5
+// written once). Measured on B200: a serving step of 64 rows, 9,934 pages 9.6
 // us; a beam step of 96 rows with 66 copies in 16 layers, 277 MB 53 us (5.2
 // TB/s); a compaction of 700 pages in 8 layers, 1.47 GB 245 us (6.0 TB/s, 0.91
 // of the measured copy rate); a compaction of 20 small pages 6.4 us, the host's
