@@ -1361,8 +1361,10 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
         for (int h = 0; h < GPT; ++h) {
           const int hg = h0 + h;
           if (hg < rows && dim < (PAGED ? p.cache.d : D)) {
-            const float ov = tot[h] > 0.f ? __uint_as_float(o[h]) / tot[h] : 0.f;
-            const float l2 = tot[h] > 0.f ? m[h] + lg2_approx(tot[h]) : -INFINITY;
+            // (tot = 0: no key, or every score -inf. A NaN score, or an infinite one,
+            // makes tot NaN, which goes on into o, lse and the gather.)
+            const float ov = tot[h] == 0.f ? 0.f : __uint_as_float(o[h]) / tot[h];
+            const float l2 = tot[h] == 0.f ? -INFINITY : m[h] + lg2_approx(tot[h]);
             if (piece_whole) {
               // The whole segment lay in this CTA: this is the result.
               if constexpr (PAGED) {
@@ -1476,7 +1478,7 @@ __global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p
   float mx = -INFINITY, tot = 0.f;
   float acc[EPL] = {};
   auto fold = [&](float lse, const float (&x)[EPL]) {
-    if (lse == -INFINITY) return;
+    if (lse == -INFINITY) return;  // (saw no key; a NaN goes into the sums)
     const float nm = fmaxf(mx, lse);
     const float sc = ex2_approx(mx - nm);  // mx = -inf gives 0
     const float wt = ex2_approx(lse - nm);
@@ -1496,7 +1498,7 @@ __global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p
     for (int e = 0; e < EPL; ++e) xr[e] = x[e];
     fold(p.part_lse[slot], xr);
   }
-  const float inv = tot > 0.f ? 1.f / tot : 0.f;
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;
   long long orow = row;
   int cols = D;
   if constexpr (PAGED) {
@@ -1514,7 +1516,7 @@ __global__ void __launch_bounds__(128) attn_decode_gather_kernel(const PParams p
   else
     *reinterpret_cast<uint32_t*>(dst) = pk[0];
   if (lane == 0 && p.lse != nullptr)
-    p.lse[orow] = tot > 0.f ? (mx + lg2_approx(tot)) * 0.69314718055994531f : -INFINITY;
+    p.lse[orow] = tot == 0.f ? -INFINITY : (mx + lg2_approx(tot)) * 0.69314718055994531f;
 }
 
 }  // namespace decode_ps

@@ -120,7 +120,9 @@ __global__ void __launch_bounds__(generic::kThreads) attn_paged_generic_kernel(c
       const int key = kv0 + lane;
       x = (key >= lo && key <= pos) ? x * p.scale_log2 : -INFINITY;
       const float m_new = fmaxf(m[i], generic::warp_max(x));
-      if (m_new == -INFINITY) continue;  // no visible key for this row yet
+      // No visible key for this row yet, or none whose score is above -inf. (The
+      // maximum leaves NaN out; such scores go into the sum, which they make NaN.)
+      if (m_new == -INFINITY && !__any_sync(0xffffffffu, isnan(x))) continue;
       const float alpha = exp2f(m[i] - m_new);  // m = -inf gives 0
       const float pj = exp2f(x - m_new);
       l[i] = l[i] * alpha + generic::warp_sum(pj);
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(generic::kThreads) attn_paged_generic_kernel(c
   for (int i = 0; i < kRowsPerWarp; ++i) {
     const long long r = r0 + warp * kRowsPerWarp + i;
     if (r >= rows) continue;
-    const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
     const size_t token = static_cast<size_t>(s.q0 + r / p.G);
     if (lane < nchunk) {
       uint4 w;
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(generic::kThreads) attn_paged_generic_kernel(c
     }
     if (lane == 0 && p.lse != nullptr)
       p.lse[token * p.Hq + g * p.G + r % p.G] =
-          l[i] > 0.f ? (m[i] + log2f(l[i])) * 0.69314718055994531f : -INFINITY;
+          l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
   }
 }
 

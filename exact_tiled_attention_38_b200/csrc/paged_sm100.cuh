@@ -1160,7 +1160,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_ok = r < p.tt * p.G && tok < w.s.T;
       if (__any_sync(0xffffffffu, row_ok)) {
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        // (l = 0: no key, or every score -inf. A NaN score, or an infinite one, makes l
+        // NaN, which goes on into o, lse and the gather.)
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         w0 *= inv;
         w1 *= inv;
         // 32 columns of the row's O, normalised; zeros for a row without keys
@@ -1179,7 +1181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) f[e] = fmaf(__uint_as_float(o[e]), w1, f[e]);
           }
-          if (l <= 0.f) {
+          if (l == 0.f) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) f[e] = 0.f;
           }
@@ -1187,7 +1189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (The loops over columns stay loops: this code runs once a piece, often on
         // a cold instruction cache; unrolled, 8K tokens took 497 us where they took
         // 479.)
-        const float l2 = l > 0.f ? m + lg2_approx(l) : -INFINITY;
+        const float l2 = l == 0.f ? -INFINITY : m + lg2_approx(l);
         if (w.whole()) {
           // Each thread writes its own row, a 32-byte sector at a time. (Through
           // shared memory, in whole lines, it took twice as long.)
@@ -1305,7 +1307,7 @@ __global__ void __launch_bounds__(256) attn_paged_gather_kernel(const Params p) 
     float4 x[CW];
 #pragma unroll
     for (int u = 0; u < CW; ++u) x[u] = src[(warp + 8 * u) * 32];
-    if (lse == -INFINITY) continue;
+    if (lse == -INFINITY) continue;  // (saw no key; a NaN goes into the sums)
     const float nm = fmaxf(mx, lse);
     const float sc = ex2_approx(mx - nm), wt = ex2_approx(lse - nm);
     tot = tot * sc + wt;
@@ -1318,7 +1320,7 @@ __global__ void __launch_bounds__(256) attn_paged_gather_kernel(const Params p) 
     }
     mx = nm;
   }
-  const float inv = tot > 0.f ? 1.f / tot : 0.f;
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;
 #pragma unroll
   for (int u = 0; u < CW; ++u) {
     uint2 v;
@@ -1333,7 +1335,7 @@ __global__ void __launch_bounds__(256) attn_paged_gather_kernel(const Params p) 
   };
   long long orow;
   if (warp == 0 && p.lse != nullptr && out_row(lane, orow))
-    p.lse[orow] = tot > 0.f ? (mx + lg2_approx(tot)) * 0.69314718055994531f : -INFINITY;
+    p.lse[orow] = tot == 0.f ? -INFINITY : (mx + lg2_approx(tot)) * 0.69314718055994531f;
   __syncthreads();
   for (int i = threadIdx.x; i < 32 * D / 8; i += 256) {
     const int q = i / (D / 8), u = i % (D / 8);

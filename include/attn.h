@@ -309,6 +309,9 @@ typedef struct attn_pages {
  * The keys and values of the new tokens must be in the cache already
  * (attn_rope_append puts them there). A token that sees no key gets o = 0,
  * lse = -inf; rows of o and lse outside every sequence are left as they were.
+ * A NaN or +infinite score at a key that a token sees makes its o and lse NaN;
+ * keys with a score of -infinity do not count, and a token that sees no other
+ * key is one that sees none.
  * What pages hold behind L_b is not looked at, NaN and infinities included.
  * Inside L_b they count as values: the value product runs over whole tiles of
  * 128 keys, so an infinite or NaN v at a position that a token does not see
