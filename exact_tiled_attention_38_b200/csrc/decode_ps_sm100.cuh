@@ -55,8 +55,9 @@
 // that begin where the cache's do (16-byte copies whose addresses went through
 // the page table kept the ring waiting: 283 us on the ragged batch below, 195
 // us by TMA, 0.95 of the measured copy rate); rows of V behind a sequence's
-// last key are set to zero before the product; a cut segment's partials go to
-// two slots a CTA. 4 sequences of 30-700 tokens, 32/8 heads: 9.8 us, of which
+// last key, and in front of the first one that a token sees, are set to zero
+// before the product, and pages wholly in front of that one are not looked up;
+// a cut segment's partials go to two slots a CTA. 4 sequences of 30-700 tokens, 32/8 heads: 9.8 us, of which
 // 6 us are the chain start, plan, page id, K, scores, V, output, and 3 us the
 // gather's.
 //
@@ -264,7 +265,7 @@ __device__ __forceinline__ SeqKeys seq_keys(const PParams& p, int b) {
     s.T = q.T;
     s.len = q.T > 0 ? q.L : 0;
     // (tiles begin where the cache's do, so that whole pages fall into a tile)
-    s.k0 = p.window > 0 ? min(max(0, q.L - q.T - p.window + 1), max(s.len - 1, 0)) & ~(TK - 1) : 0;
+    s.k0 = min(paged::first_seen(q, 0, p.window), max(s.len - 1, 0)) & ~(TK - 1);
   } else {
     s.q0 = 0;
     s.T = 1;
@@ -472,6 +473,10 @@ struct Cursor {
     } while (nt == 0 && b < p.B - 1);
   }
   __device__ __forceinline__ int segment(const PParams& p) const { return b * p.Hkv + g; }
+  // PAGED: the first key that any of the sequence's new tokens sees.
+  __device__ __forceinline__ int seen_from(const PParams& p) const {
+    return paged::first_seen(paged::Seq{q0, T, len}, 0, p.window);
+  }
 };
 
 template <int NP, int D>
@@ -941,12 +946,13 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
       // PAGED: lane l copies page l / boxes of the tile, 64 columns of it, by
       // one TMA load; its page id is read while the stage is still in use.
       // What the sequence does not have (pages behind its last, or an id
-      // outside the pool) is loaded out of range: zeros, nothing is read.
+      // outside the pool) and what no token sees (pages in front of the window)
+      // is loaded out of range: zeros, nothing is read.
       [[maybe_unused]] int page = 0;
       if constexpr (PAGED) {
         const int key = cur.k0 + cur.i * TK + (lane / C::kBoxes) * box_rows;
         page = p.cache.num_pages;
-        if (lane < lanes && key < cur.len) {
+        if (lane < lanes && key < cur.len && key + box_rows > cur.seen_from(p)) {
           const int id = p.cache.table[static_cast<size_t>(cur.b) * p.cache.width +
                                        (key >> p.cache.page_log2)];
           if (id >= 0 && id < p.cache.num_pages)
@@ -1075,7 +1081,9 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
     bool ok = true;
     int k = -1;                // current piece
     bool prev_first = false;   // tile j - 1 started its piece
-    [[maybe_unused]] int prev_keys = TK;  // PAGED: keys of tile j - 1
+    [[maybe_unused]] int prev_keys = TK;  // PAGED: keys of tile j - 1,
+    [[maybe_unused]] int prev_front = 0;  // and how many of them no token sees
+    [[maybe_unused]] const int box_rows = PAGED ? min(1 << p.cache.page_log2, TK) : TK;
     uint32_t qb = 0;
     for (int j = 0; ok && j <= n; ++j) {
       if (j < n) {
@@ -1131,15 +1139,20 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
                   wait_bar_spin(&full_v[st], (jp / kStages) & 1, ctl, kSiteFull))))
           break;
         if constexpr (PAGED) {
-          // Rows of V behind the sequence's last key: zeros, whatever lies in
-          // the pool there (their probabilities are zero, but 0 * NaN is not).
-          if (prev_keys < TK) {
+          // Rows of V behind the sequence's last key, and of the first page needed
+          // in front of the first key seen: zeros, whatever lies in the pool there
+          // (their probabilities are zero, but 0 * NaN is not).
+          if (prev_keys < TK || prev_front > 0) {
             uint8_t* vt = smem + st * C::kStageBytes + C::kTileBytes;
-            for (int i = lane; i < (TK - prev_keys) * C::kBoxes * 8; i += 32) {
-              const int row = prev_keys + (i >> 3) / C::kBoxes, box = (i >> 3) % C::kBoxes;
-              *reinterpret_cast<uint4*>(vt + box * C::kBoxBytes + row * 128 + (i & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
+            auto clear = [&](int from, int to) {
+              for (int i = lane; i < (to - from) * C::kBoxes * 8; i += 32) {
+                const int row = from + (i >> 3) / C::kBoxes, box = (i >> 3) % C::kBoxes;
+                *reinterpret_cast<uint4*>(vt + box * C::kBoxBytes + row * 128 + (i & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+              }
+            };
+            clear(prev_keys, TK);
+            clear(max(prev_front, 0) & ~(box_rows - 1), prev_front);
             __syncwarp();
           }
         }
@@ -1162,7 +1175,10 @@ __global__ void __launch_bounds__(Roles<HS>::kThreads, 1)
       }
       if (j < n) {
         prev_first = (j == 0) || (cur.i == 0);
-        if constexpr (PAGED) prev_keys = cur.len - (cur.k0 + cur.i * TK);
+        if constexpr (PAGED) {
+          prev_keys = cur.len - (cur.k0 + cur.i * TK);
+          prev_front = cur.seen_from(p) - (cur.k0 + cur.i * TK);
+        }
         if (j + 1 < n) cur.next(p);
       }
     }

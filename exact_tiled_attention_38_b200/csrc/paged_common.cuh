@@ -75,6 +75,11 @@ __device__ __forceinline__ Seq load_seq(const int* __restrict__ cu_q, const int*
   return s;
 }
 
+// The first key that new token t of the sequence, and so any from t on, sees.
+__device__ __forceinline__ int first_seen(const Seq& s, int t, int window) {
+  return window > 0 ? max(0, s.L - s.T + t - window + 1) : 0;
+}
+
 // Records what load_seq() had to clamp (called once per sequence).
 __device__ __forceinline__ void check_seq(const int* __restrict__ cu_q,
                                           const int* __restrict__ lens, int b, int total_q,

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(generic::kThreads) attn_paged_generic_kernel(c
   }
   const long long rl = min(r0 + kRows, rows) - 1;
   const int khi = min(off + static_cast<int>(rl / p.G), s.L - 1);
-  const int klo = p.window > 0 ? max(0, off + static_cast<int>(r0 / p.G) - p.window + 1) : 0;
+  const int klo = first_seen(s, static_cast<int>(r0 / p.G), p.window);  // (for any row here)
 
   float m[kRowsPerWarp], l[kRowsPerWarp], o[kRowsPerWarp][8];
 #pragma unroll
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(generic::kThreads) attn_paged_generic_kernel(c
       const int j = i / nchunk, u = i - j * nchunk;
       const int key = kv0 + j;
       uint4 kv = make_uint4(0u, 0u, 0u, 0u), vv = kv;
-      if (key < s.L) {
+      if (key >= klo && key < s.L) {
         const int page = table[key >> c.page_log2];
         if (page >= 0 && page < c.num_pages) {
           const size_t at = page * c.page_stride + g * c.head_stride +

@@ -63,9 +63,11 @@
 // sustained rate); 9 sequences of up to 301 tokens under a window of 4096, 16/2
 // heads, d = 64 55 us.
 //
-// Rows of V behind the sequence's last key are set to zero in shared memory
-// before the product: their probabilities are zero, but what lies there in the
-// pool may be infinite or NaN.
+// Rows of V behind the sequence's last key, and under a window those in front
+// of the first key that any row of the item sees, are set to zero in shared
+// memory before the product: their probabilities are zero, but what lies there
+// in the pool may be infinite or NaN. Pages wholly in front of that key are not
+// looked up (the cache may have given them up).
 #pragma once
 
 #include "paged_common.cuh"
@@ -190,9 +192,9 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const Params& p, const Seq& s, int pair) {
   const int t0 = pair * NQT * p.tt, t1 = min(s.T, t0 + NQT * p.tt);
-  const int last = s.L - s.T + t1 - 1, first = s.L - s.T + t0;
+  const int last = s.L - s.T + t1 - 1;
   Span r;
-  r.lo = p.window > 0 ? max(0, first - p.window + 1) / BN : 0;
+  r.lo = first_seen(s, t0, p.window) / BN;
   r.n = last < 0 ? 1 : max(1, last / BN + 1 - r.lo);
   if (last < 0) r.lo = 0;
   return r;
@@ -618,6 +620,10 @@ struct Walk {
   __device__ __forceinline__ int slot(int c, int nc) const {
     return c < chunks || i0 != first ? c : i1 < n ? nc + c : 2 * nc + chunk;
   }
+  // The first key that any row of the item sees.
+  __device__ __forceinline__ int seen_from(const Params& p) const {
+    return first_seen(s, pair * NQT * p.tt, p.window);
+  }
   // Both tiles have rows?
   __device__ __forceinline__ bool two(const Params& p) const {
     return pair * NQT * p.tt + p.tt < s.T;
@@ -780,14 +786,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++qn[t];
       }
       // The page that this lane loads of key tile j: its id, or num_pages
-      // (out of range: zeros) where the sequence has none.
+      // (out of range: zeros) where the sequence has none or no row sees any of it.
       const int* row = p.table + static_cast<size_t>(w.b) * p.width;
-      const int keys = w.s.L, g = w.head, n = w.steps();
+      const int keys = w.s.L, seen = w.seen_from(p), g = w.head, n = w.steps();
       const int j0 = w.lo + w.i0;
       int at = w.rot;  // step of the piece
       auto page_of = [&](int j) {
         const int key = j * BN + pg * box_rows;
-        if (!loads || key >= keys) return p.num_pages;
+        if (!loads || key >= keys || key + box_rows <= seen) return p.num_pages;
         const int id = row[key >> p.page_log2];
         if (id >= 0 && id < p.num_pages) return id;
         bad(kBadPage);
@@ -874,20 +880,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_ts_w<1>(tO, tP + kk * 8, desc_words(vd + kk * 128, d_hi), idesc_pv);
       if constexpr (C::kOwnP) umma_commit_w(&pv_done[t]);
     };
-    // Rows of V behind the sequence's last key: zeros (the pages behind it are
-    // zeros already; those of its last page may hold anything).
+    // Rows of V behind the sequence's last key and in front of the first one seen:
+    // zeros (the other pages there are zeros already; those of the last page, and
+    // of the first one needed, may hold anything).
     int tail = 0, rot = 0, n = 0;  // keys of the sequence from the piece's first key tile on
-    auto clear_tail = [&](int j, uint32_t lv) {
-      const int valid = tail - (j + rot < n ? j + rot : j + rot - n) * BN;
-      if (valid >= BN) return;
-      const int from = max(valid, 0);
+    int front = 0;                 // those of them that no row sees
+    const int box_rows = min(1 << p.page_log2, BN);
+    auto clear_ends = [&](int j, uint32_t lv) {
+      const int t0 = (j + rot < n ? j + rot : j + rot - n) * BN;  // (the piece's key tile)
+      const int valid = tail - t0, unseen = front - t0;
+      if (valid >= BN && unseen <= 0) return;
       uint8_t* base = sKV + (lv % S) * C::kTileBytes;
-      for (int i = lane; i < (BN - from) * C::kBoxes * 8; i += 32) {
-        const int u = i & 7, rb = i >> 3;
-        const int r = from + rb / C::kBoxes, x = rb % C::kBoxes;
-        *reinterpret_cast<uint4*>(base + x * C::kBoxBytes + r * 128 + u * 16) =
-            make_uint4(0u, 0u, 0u, 0u);
-      }
+      auto clear = [&](int from, int to) {
+        for (int i = lane; i < (to - from) * C::kBoxes * 8; i += 32) {
+          const int u = i & 7, rb = i >> 3;
+          const int r = from + rb / C::kBoxes, x = rb % C::kBoxes;
+          *reinterpret_cast<uint4*>(base + x * C::kBoxBytes + r * 128 + u * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+      };
+      clear(max(valid, 0), BN);
+      clear(max(unseen, 0) & ~(box_rows - 1), unseen);
       fence_proxy_async_smem();
       __syncwarp();
     };
@@ -895,6 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       n = w.steps();
       rot = w.rot;
       tail = w.s.L - (w.lo + w.i0) * BN;
+      front = w.seen_from(p) - (w.lo + w.i0) * BN;
       if (w.two(p)) {
         for (int j = 0; ok && j <= n; ++j) {
           const uint32_t Lk = L + 2 * j, Lv = L + 2 * j - 1;
@@ -917,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j < 1 || !ok) return;
             if (t == 0) {
               if (!(ok = warp_all(wait_bar(&kv_full[Lv % S], (Lv / S) & 1, ctl, kSiteKvFull)))) return;
-              clear_tail(j - 1, Lv);
+              clear_ends(j - 1, Lv);
             }
             if (!(ok = warp_all(wait_bar(&p_ready[t], pw[t] & 1, ctl, kSitePReady)))) return;
             ++pw[t];
@@ -959,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int t = (j - 1) & 1;
             const uint32_t Lv = L + 2 * j - 1;
             if (!(ok = warp_all(wait_bar(&kv_full[Lv % S], (Lv / S) & 1, ctl, kSiteKvFull)))) break;
-            clear_tail(j - 1, Lv);
+            clear_ends(j - 1, Lv);
             if (!(ok = warp_all(wait_bar(&p_ready[t], pw[t] & 1, ctl, kSitePReady)))) break;
             ++pw[t];
             tc_fence_after();

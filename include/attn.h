@@ -312,9 +312,12 @@ typedef struct attn_pages {
  * A NaN or +infinite score at a key that a token sees makes its o and lse NaN;
  * keys with a score of -infinity do not count, and a token that sees no other
  * key is one that sees none.
- * What pages hold behind L_b is not looked at, NaN and infinities included.
- * Inside L_b they count as values: the value product runs over whole tiles of
- * 128 keys, so an infinite or NaN v at a position that a token does not see
+ * What pages hold behind L_b, and in front of the first position that any new
+ * token of the sequence sees under a window, is not looked at, NaN and
+ * infinities included; pages wholly in front of it are not needed, and their
+ * table entries may hold anything (-1, say, once the page serves another row).
+ * Between the two they count as values: the value product runs over whole tiles
+ * of 128 keys, so an infinite or NaN v at a position that a token does not see
  * may still reach it where other tokens see it (d <= 128).
  * d <= 128 with at most 128 query heads per KV head runs on the tensor cores
  * (any d below 64 or 128 at the cost of that size), other sizes on a CUDA-core
