@@ -167,6 +167,15 @@ __device__ __forceinline__ int ceil_pages(int len, int log2) {
   return static_cast<int>((static_cast<long long>(len) + (1 << log2) - 1) >> log2);
 }
 
+// Is there a page? An entry of -1 inside a row is one that the row has given up
+// (a page in front of a sliding window); any other id outside the pool is
+// reported. Neither is followed.
+__device__ __forceinline__ bool held_page(int page, const Params& p) {
+  if (page >= 0 && page < p.P) return true;
+  if (page != -1) paged::bad(paged::kBadPage);
+  return false;
+}
+
 // One row of an update: what it goes on from and what it keeps.
 struct Row {
   int s;      // source row, -1: none
@@ -228,10 +237,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int j = lane; j < n; j += 32) {
       const int page = p.table[static_cast<size_t>(b) * p.width + j];
-      if (page >= 0 && page < p.P)
-        atomicAdd(p.refs_out + page, -1);
-      else
-        paged::bad(paged::kBadPage);
+      if (held_page(page, p)) atomicAdd(p.refs_out + page, -1);
     }
   }
   cluster_barrier();
@@ -386,10 +392,12 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
       int page = -1;
       if (j < held) {
         page = p.table[e];
-        if (page < 0 || page >= p.P || p.refs[page] <= 0)
-          paged::bad(paged::kBadPage);  // (left as it was)
-        else if (page >= n)
-          page = ld(p.to + ld(p.list + page));
+        if (held_page(page, p)) {
+          if (p.refs[page] <= 0)
+            paged::bad(paged::kBadPage);  // (left as it was)
+          else if (page >= n)
+            page = ld(p.to + ld(p.list + page));
+        }
       }
       p.table_out[e] = page;
     }
@@ -498,10 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = lane; j < held; j += 32) {
       const int d = j < full ? k - 1 : k > 0 ? 0 : -1;
       const int page = p.table[static_cast<size_t>(b) * p.width + j];
-      if (page < 0 || page >= p.P)
-        paged::bad(paged::kBadPage);
-      else if (d != 0)
-        atomicAdd(refs + page, d);
+      if (held_page(page, p) && d != 0) atomicAdd(refs + page, d);
     }
   }
   // What each row keeps and needs, a few rows a thread.
@@ -543,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       page = p.table[row + j];
     } else if (j < kept[b]) {
       page = p.table[static_cast<size_t>(max(src[b], 0)) * p.width + j];
-      if (page < 0 || page >= p.P) paged::bad(paged::kBadPage);
+      held_page(page, p);  // (reports a bad one)
     } else if (j < ceil_pages(longer[b], p.page_log2)) {
       page = list[first[b] + j - kept[b]];
     }
@@ -566,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       [&](int b) { return src[b] >= 0 && ceil_pages(len[src[b]], p.page_log2) > kept[b]; },
       [&](int b, int k) {
         const int of = p.table[static_cast<size_t>(src[b]) * p.width + kept[b]], page = list[first[b]];
-        from[k] = of >= 0 && of < p.P ? of : page;  // (a bad id was reported: nothing to copy)
+        from[k] = of >= 0 && of < p.P ? of : page;  // (no page there: nothing to copy)
         to[k] = page;
       });
   __syncthreads();
@@ -620,10 +625,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     int page = -1;
     if (j < ceil_pages(L, p.page_log2)) {
       page = p.table[e];
-      if (page < 0 || page >= p.P || p.refs[page] <= 0)
-        paged::bad(paged::kBadPage);  // (left as it was)
-      else if (page >= n)
-        page = ~refs[page];
+      if (held_page(page, p)) {
+        if (p.refs[page] <= 0)
+          paged::bad(paged::kBadPage);  // (left as it was)
+        else if (page >= n)
+          page = ~refs[page];
+      }
     }
     p.table_out[e] = page;
   }

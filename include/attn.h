@@ -425,7 +425,10 @@ int attn_rope_turns(double* turns, float* amp, int rot, double base, int scaling
  *     first, in the order of the rows.
  *   lens, refs, source, add: [B], [num_pages], [B], [B] int32; refs[p] counts
  *        the rows that hold page p (and whoever else pins it). A row of L
- *        tokens holds its first ceil(L / page_size) table entries.
+ *        tokens holds its first ceil(L / page_size) table entries. An entry of
+ *        -1 among them is a page that the row has given up and stays -1: the
+ *        caller gives up a full page (in front of a sliding window, say) by
+ *        setting the entry to -1 and taking 1 off the page's count.
  *   table_out, lens_out, refs_out: the next state (entries behind a row's pages
  *        are -1). They must not be the inputs.
  *   info [2] int32: pages that were missing, and rows longer than the table

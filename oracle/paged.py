@@ -121,7 +121,8 @@ def update_ref(table, lens, refs, source, add, page):
     up = lambda n: -(-n // page)  # noqa: E731
     for b in range(B):
         for p in table[b][:up(lens[b])]:
-            count[p] -= 1
+            if p >= 0:  # (-1: given up)
+                count[p] -= 1
     keeper = {}
     for b, s in enumerate(source):
         if s >= 0 and (s == b or s not in keeper):
@@ -132,7 +133,8 @@ def update_ref(table, lens, refs, source, add, page):
             for b, s in enumerate(source)]
     for b, s in enumerate(source):
         for p in (table[s][:kept[b]] if s >= 0 else []):
-            count[p] += 1
+            if p >= 0:
+                count[p] += 1
     free = [p for p, c in enumerate(count) if c <= 0]
     long_rows = sum(up(n) > width for n in longer)
     need = sum(up(longer[b]) - kept[b] for b in range(B) if up(longer[b]) <= width)
