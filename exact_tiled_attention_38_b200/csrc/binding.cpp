@@ -175,27 +175,36 @@ int rotated(const at::Tensor& turns, int dev, int64_t d) {
   return static_cast<int>(2 * turns.size(0));
 }
 
-// The device made current, and the stream: None is the current one.
+// The device made current, and the stream: None is the current one. A given
+// stream is made current too, so that outputs allocated here come from its own
+// memory: a block of the current stream's may have been freed there while work
+// queued on that stream still uses it, which the given one does not wait for.
 struct Place {
   c10::cuda::OptionalCUDAGuard guard;
+  c10::cuda::CUDAStream before;
+  c10::cuda::OptionalCUDAStreamGuard on;
   attn_stream_t stream;
-  Place(int dev, PyObject* s) : guard(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev))) {
-    if (s == Py_None)
-      stream = reinterpret_cast<attn_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream());
-    else
-      stream = reinterpret_cast<attn_stream_t>(PyLong_AsUnsignedLongLong(s));
-    given = s != Py_None;
-    device = static_cast<c10::DeviceIndex>(dev);
-  }
-  // A tensor allocated here (on the current stream) for work on another one:
-  // its memory is not handed out again before that work is done.
-  void allocated(const at::Tensor& t) const {
-    if (given && t.defined())
-      t.record_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(stream), device)
-                          .unwrap());
-  }
   bool given;
-  c10::DeviceIndex device;
+  Place(int dev, PyObject* s)
+      : guard(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev))),
+        before(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev))),
+        given(s != Py_None) {
+    stream = reinterpret_cast<attn_stream_t>(before.stream());
+    if (!given) return;
+    const unsigned long long handle = PyLong_AsUnsignedLongLong(s);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      refuse("stream must be a stream or its handle");
+    }
+    stream = reinterpret_cast<attn_stream_t>(handle);
+    on.reset_stream(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(handle),
+                                                     static_cast<c10::DeviceIndex>(dev)));
+  }
+  // A tensor allocated here for a caller on the stream that was current: its
+  // memory is not handed out again before that stream's work with it is done.
+  void allocated(const at::Tensor& t) const {
+    if (given && t.defined()) t.record_stream(before.unwrap());
+  }
 };
 
 template <typename F, typename... A>
