@@ -11,6 +11,104 @@ constexpr int kMaxPackedRows = 1 << 29;
 
 inline bool mult8(long long x) { return (x & 7) == 0; }
 
+// ------------------------------------------------------------------ overlaps
+// Outputs are written while inputs are still read by other CTAs, so an output
+// that lies over an input (but for the in-place forms) or over another output
+// is refused.
+
+inline long long gap(const void* from, const void* to) {  // bytes
+  return static_cast<long long>(reinterpret_cast<intptr_t>(to) - reinterpret_cast<intptr_t>(from));
+}
+
+// Blocks of na and nb bytes.
+inline bool blocks_meet(const void* a, long long na, const void* b, long long nb) {
+  const long long g = gap(a, b);
+  return na > 0 && nb > 0 && g < na && g > -nb;
+}
+
+// Pieces of d elements (of 2 bytes) at base + i . s, 0 <= i < n.
+struct Grid {
+  const void* base;
+  long long n[3], s[3];
+  long long d;
+  bool empty() const { return n[0] <= 0 || n[1] <= 0 || n[2] <= 0 || d <= 0; }
+  // Elements from the first to behind the last; a dimension of one has no stride.
+  double extent() const {
+    double e = static_cast<double>(d);
+    for (int k = 0; k < 3; ++k) e += static_cast<double>(n[k] - 1) * static_cast<double>(n[k] > 1 ? s[k] : 0);
+    return e;
+  }
+  // No memory is that large (and within it the arithmetic below stays in 64 bits).
+  bool too_large() const { return !empty() && extent() > 0x1p46; }
+};
+
+// Do two of a grid's own pieces overlap? (Also where its strides do not nest, so
+// that it would take a search to tell.)
+inline bool grid_meets_itself(const Grid& a) {
+  if (a.empty()) return false;
+  int by[3] = {0, 1, 2};  // ascending strides
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (a.s[by[j]] > a.s[by[j + 1]]) std::swap(by[j], by[j + 1]);
+  long long extent = a.d;
+  for (int k : by) {
+    if (a.n[k] <= 1) continue;
+    if (a.s[k] < extent) return true;
+    extent += (a.n[k] - 1) * a.s[k];
+  }
+  return false;
+}
+
+// Are there whole numbers x[k] in [range[k][0], range[k][1]] with
+// -below < at + x . s < above? Strides descend.
+inline bool steps_reach(long long at, int dims, const long long (*range)[2], const long long* s,
+                        long long below, long long above) {
+  if (dims == 0) return at > -below && at < above;
+  long long rest = 0;  // how far the other dimensions go
+  for (int k = 1; k < dims; ++k) rest += s[k] * std::max(-range[k][0], range[k][1]);
+  const auto floor_div = [](long long a, long long b) { return a >= 0 ? a / b : -((-a + b - 1) / b); };
+  const long long lo = std::max(range[0][0], -floor_div(below - 1 + rest + at, s[0]));
+  const long long hi = std::min(range[0][1], floor_div(above - 1 + rest - at, s[0]));
+  if (hi - lo > 7) return true;  // (strides that do not nest: taken to meet)
+  for (long long x = lo; x <= hi; ++x)
+    if (steps_reach(at + x * s[0], dims - 1, range + 1, s + 1, below, above)) return true;
+  return false;
+}
+
+// Do two grids overlap? Exact for parts of one tensor (equal strides, which
+// nest); others are taken to if the memory between their ends does.
+inline bool grids_meet(const Grid& a, const Grid& b) {
+  if (a.empty() || b.empty() || !blocks_meet(a.base, 2 * static_cast<long long>(a.extent()), b.base,
+                                             2 * static_cast<long long>(b.extent())))
+    return false;
+  long long s[3], range[3][2];
+  int dims = 0;
+  for (int k = 0; k < 3; ++k) {
+    if (a.n[k] <= 1 && b.n[k] <= 1) continue;
+    if (a.n[k] > 1 && b.n[k] > 1 && a.s[k] != b.s[k]) return true;
+    const long long stride = a.n[k] > 1 ? a.s[k] : b.s[k];
+    if (stride == 0) continue;  // (an input that is the same along this dimension)
+    int at = dims++;
+    for (; at > 0 && s[at - 1] < stride; --at) {
+      s[at] = s[at - 1];
+      range[at][0] = range[at - 1][0];
+      range[at][1] = range[at - 1][1];
+    }
+    s[at] = stride;
+    range[at][0] = -(a.n[k] - 1);
+    range[at][1] = b.n[k] - 1;
+  }
+  return steps_reach(gap(a.base, b.base) / 2, dims, range, s, b.d, a.d);
+}
+
+// The same places, piece for piece (in place)?
+inline bool grids_equal(const Grid& a, const Grid& b) {
+  if (a.base != b.base) return false;
+  for (int k = 0; k < 3; ++k)
+    if (a.n[k] > 1 && a.s[k] != b.s[k]) return false;
+  return true;
+}
+
 // The cache as the kernels see it; ATTN_OK or the error of a bad description
 // (a batch of no sequences has no table).
 inline int cache_of(const attn_pages* c, int B, paged::Cache* out) {
@@ -224,6 +322,13 @@ int paged_run(const void* q, long long q_stride, const attn_pages* pages, const 
       !aligned(o, 16) || !aligned(cu_q, 4) || !aligned(kv_lens, 4) ||
       (lse != nullptr && !aligned(lse, 4)))
     return ATTN_ERR_INVALID;
+  const long long heads = static_cast<long long>(total_q) * Hq;
+  const Grid q_rows{q, {total_q, 1, 1}, {q_stride, 0, 0}, static_cast<long long>(Hq) * c.d};
+  const auto block = [](const void* at, long long bytes) { return Grid{at, {1, 1, 1}, {0, 0, 0}, bytes / 2}; };
+  const Grid o_all = block(o, heads * c.d * 2), lse_all = block(lse, lse != nullptr ? heads * 4 : 0);
+  if (q_rows.too_large() || grids_meet(o_all, q_rows) || grids_meet(lse_all, q_rows) ||
+      grids_meet(o_all, lse_all))
+    return ATTN_ERR_INVALID;
   DeviceInfo info;
   if (device_info(&info) != ATTN_OK) return ATTN_ERR_CUDA;
   if (!info.sm100) return ATTN_ERR_UNSUPPORTED;
@@ -406,12 +511,22 @@ int rope_run(const void* q, void* q_out, const void* k, void* k_out, const long 
   p.sign = backward ? -1.f : 1.f;
   p.N = N;
   p.tokens = static_cast<long long>(B) * N;
+  const auto grid = [&](const void* base, int H, const long long* st) {
+    return Grid{base, {B, H, N}, {st[0], st[1], st[2]}, d};
+  };
+  const Grid qi = grid(q, Hq, s), qo = grid(q_out, Hq, s + 3), ki = grid(k, Hkv, s + 6),
+             ko = grid(k_out, Hkv, s + 9);
+  const bool q_in_place = Hq == 0 || grids_equal(qi, qo), k_in_place = Hkv == 0 || grids_equal(ki, ko);
   // In place, the values that pass through are there already.
-  const bool same = (Hq == 0 || (q == q_out && s[0] == s[3] && s[1] == s[4] && s[2] == s[5])) &&
-                    (Hkv == 0 || (k == k_out && s[6] == s[9] && s[7] == s[10] && s[8] == s[11]));
+  const bool same = q_in_place && k_in_place;
   p.d = same ? rot : d;
   p.rot = rot;
   if (p.d == 0) return ATTN_OK;
+  if (qi.too_large() || qo.too_large() || ki.too_large() || ko.too_large() || grid_meets_itself(qo) ||
+      grid_meets_itself(ko) || (!q_in_place && grids_meet(qo, qi)) ||
+      (!k_in_place && grids_meet(ko, ki)) || grids_meet(qo, ki) || grids_meet(ko, qi) ||
+      grids_meet(qo, ko))
+    return ATTN_ERR_INVALID;
   return launch_rope<T, false>(p, interleaved, st);
 }
 
@@ -441,6 +556,14 @@ int rope_append_run(const void* q, long long q_stride, void* q_out, long long q_
       (rot > 0 && (turns == nullptr || !aligned(turns, 8))) ||
       (Hq > 0 && (q == nullptr || q_out == nullptr || !aligned(q, 16) || !aligned(q_out, 16))))
     return ATTN_ERR_INVALID;
+  const auto rows = [&](const void* x, long long stride, long long row) {
+    return Grid{x, {total_q, 1, 1}, {stride, 0, 0}, row};
+  };
+  const Grid qi = rows(q, q_stride, row_q), qo = rows(q_out, q_out_stride, row_q),
+             ki = rows(k, k_stride, row_kv), vi = rows(v, v_stride, row_kv);
+  if (qi.too_large() || qo.too_large() || ki.too_large() || vi.too_large() ||
+      (!grids_equal(qi, qo) && grids_meet(qo, qi)) || grids_meet(qo, ki) || grids_meet(qo, vi))
+    return ATTN_ERR_INVALID;
   p.t[0] = {q, q_out, 0, d, q_stride, 0, d, q_out_stride};
   p.t[1] = {k, nullptr, 0, d, k_stride, 0, 0, 0};
   p.v = v;
@@ -465,9 +588,29 @@ int rope_append_run(const void* q, long long q_stride, void* q_out, long long q_
 
 // ------------------------------------------------------------------ page operations
 
-// Checks shared by update and compact; fills what both need.
+struct Block {
+  const void* at;  // (NULL: none)
+  long long bytes;
+};
+// Does an output lie over an input, or over another output?
+inline bool overlap(std::initializer_list<Block> in, std::initializer_list<Block> out) {
+  const auto meet = [](const Block& a, const Block& b) {
+    return a.at != nullptr && b.at != nullptr && blocks_meet(a.at, a.bytes, b.at, b.bytes);
+  };
+  for (const Block* o = out.begin(); o != out.end(); ++o) {
+    for (const Block& i : in)
+      if (meet(*o, i)) return true;
+    for (const Block* other = out.begin(); other != o; ++other)
+      if (meet(*o, *other)) return true;
+  }
+  return false;
+}
+
+// Checks shared by update and compact (which has no source, add and lens_out);
+// fills what both need.
 inline int pages_setup(const attn_pages* c, int layers, long long layer_stride, int B,
-                       const int32_t* lens, const int32_t* refs, int32_t* table_out,
+                       const int32_t* lens, const int32_t* refs, const int32_t* source,
+                       const int32_t* add, int32_t* table_out, int32_t* lens_out,
                        int32_t* refs_out, int32_t* info, paged::Cache* cache, pages::Params* p,
                        pages::CopyParams* cp) {
   const int rc = cache_of(c, B, cache);
@@ -477,8 +620,8 @@ inline int pages_setup(const attn_pages* c, int layers, long long layer_stride, 
     return ATTN_ERR_INVALID;
   // A page's values in one piece, heads or tokens outermost.
   const long long hs = c->head_stride, ts = c->token_stride, d = c->d;
-  const bool heads_out = (c->page_size == 1 || ts == d) && (c->Hkv == 1 || hs == c->page_size * d);
-  const bool tokens_out = (c->Hkv == 1 || hs == d) && (c->page_size == 1 || ts == c->Hkv * d);
+  const bool heads_out = ts == d && (c->Hkv == 1 || hs == c->page_size * d);
+  const bool tokens_out = (c->Hkv == 1 || hs == d) && ts == c->Hkv * d;
   if (!heads_out && !tokens_out) return ATTN_ERR_INVALID;
   const long long page = static_cast<long long>(c->Hkv) * c->page_size * d;
   if (c->page_stride < page) return ATTN_ERR_INVALID;
@@ -486,8 +629,10 @@ inline int pages_setup(const attn_pages* c, int layers, long long layer_stride, 
       refs_out == nullptr || info == nullptr || !aligned(lens, 4) || !aligned(refs, 4) || !aligned(table_out, 4) ||
       !aligned(refs_out, 4) || !aligned(info, 4))
     return ATTN_ERR_INVALID;
-  // The inputs are read while the outputs are written.
-  if ((B > 0 && table_out == c->table) || refs_out == refs) return ATTN_ERR_INVALID;
+  const long long entries = 4LL * B * c->table_width, rows = 4LL * B, counts = 4LL * c->num_pages;
+  if (overlap({{c->table, entries}, {lens, rows}, {refs, counts}, {source, rows}, {add, rows}},
+              {{table_out, entries}, {lens_out, rows}, {refs_out, counts}, {info, 8}}))
+    return ATTN_ERR_INVALID;
   p->table = c->table;
   p->lens = lens;
   p->refs = refs;
@@ -583,10 +728,10 @@ int pages_update(const attn_pages* c, int layers, long long layer_stride, const 
   paged::Cache cache;
   pages::Params p = {};
   pages::CopyParams cp = {};
-  const int rc = pages_setup(c, layers, layer_stride, B, lens, refs, table_out, refs_out, info,
-                             &cache, &p, &cp);
+  const int rc = pages_setup(c, layers, layer_stride, B, lens, refs, source, add, table_out,
+                             lens_out, refs_out, info, &cache, &p, &cp);
   if (rc != ATTN_OK) return rc;
-  if ((B > 0 && (source == nullptr || add == nullptr || lens_out == nullptr || lens_out == lens)) ||
+  if ((B > 0 && (source == nullptr || add == nullptr || lens_out == nullptr)) ||
       !aligned(source, 4) || !aligned(add, 4) || !aligned(lens_out, 4))
     return ATTN_ERR_INVALID;
   p.source = source;
@@ -601,8 +746,8 @@ int pages_compact(const attn_pages* c, int layers, long long layer_stride, const
   paged::Cache cache;
   pages::Params p = {};
   pages::CopyParams cp = {};
-  const int rc = pages_setup(c, layers, layer_stride, B, lens, refs, table_out, refs_out, info,
-                             &cache, &p, &cp);
+  const int rc = pages_setup(c, layers, layer_stride, B, lens, refs, nullptr, nullptr, table_out,
+                             nullptr, refs_out, info, &cache, &p, &cp);
   if (rc != ATTN_OK) return rc;
   return pages_launch<false>(p, cp, st);
 }

@@ -304,6 +304,7 @@ typedef struct attn_pages {
  *   q    [total_q][Hq][d], rows of tokens q_stride elements apart (a multiple
  *        of 8, >= Hq * d: q may be a part of a wider projection)
  *   o    [total_q][Hq][d] contiguous     lse [total_q][Hq] float32, or NULL
+ *        (neither over q nor over the other: ATTN_ERR_INVALID)
  *   max_q: no sequence has more new tokens than this.
  *   window: 0 for none.
  * The keys and values of the new tokens must be in the cache already
@@ -348,7 +349,10 @@ int attn_paged_f16(const void* q, long long q_stride, const attn_pages* cache, c
  *   q, q_out [B, Hq, N, d] and k, k_out [B, Hkv, N, d], by strides in elements:
  *        strides[0..2] batch, head, token of q, [3..5] of q_out, [6..8] of k,
  *        [9..11] of k_out (HOST memory; multiples of 8; d contiguous). An
- *        output may be its input (same pointer, same strides). Hq or Hkv may be 0.
+ *        output may be its input (same pointer, same strides); else it must not
+ *        lie over an input or the other output, and its own strides must nest,
+ *        so that no two of its values share a place (ATTN_ERR_INVALID; exact for
+ *        parts of one tensor). Hq or Hkv may be 0.
  *   pos  int32, DEVICE: pos[b * pos_stride + n] (pos_stride 0: shared)
  *   turns [rot / 2] float64, DEVICE (attn_rope_turns computes them)
  * Sizes: d a multiple of 8 in [8, 256], rot even in [0, d], Hq + Hkv <= 65,535,
@@ -369,7 +373,8 @@ int attn_rope_f16(const void* q, void* q_out, const void* k, void* k_out, const 
  * new tokens' q is rotated into q_out, k is rotated into the cache, v is copied
  * into it.
  *   q, q_out [total_q][Hq][d], k, v [total_q][Hkv][d], rows of tokens *_stride
- *        elements apart (multiples of 8, at least a row); q_out may be q.
+ *        elements apart (multiples of 8, at least a row); q_out may be q (with
+ *        its stride), and must not lie over q, k or v otherwise.
  *   pos  [total_q] int32, DEVICE, or NULL: the tokens' positions in the cache.
  * A token at a negative position (T_b > L_b) is not stored. rot = 0 appends
  * without rotating. Pages that several sequences share must not be written:
@@ -430,7 +435,7 @@ int attn_rope_turns(double* turns, float* amp, int rot, double base, int scaling
  *        caller gives up a full page (in front of a sliding window, say) by
  *        setting the entry to -1 and taking 1 off the page's count.
  *   table_out, lens_out, refs_out: the next state (entries behind a row's pages
- *        are -1). They must not be the inputs.
+ *        are -1). No output may lie over an input or another output.
  *   info [2] int32: pages that were missing, and rows longer than the table
  *        allows. If either is not 0 nothing has changed: the outputs are the
  *        inputs, and no page was copied.
