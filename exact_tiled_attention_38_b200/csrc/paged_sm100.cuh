@@ -899,8 +899,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_uint4(0u, 0u, 0u, 0u);
         }
       };
-      clear(max(valid, 0), BN);
-      clear(max(unseen, 0) & ~(box_rows - 1), unseen);
+      if (valid < BN) clear(max(valid, 0), BN);
+      if (unseen > 0) clear(unseen & ~(box_rows - 1), unseen);
       fence_proxy_async_smem();
       __syncwarp();
     };
