@@ -100,7 +100,7 @@ struct Cache {
   int type, dev, B;
   int layers;  // 0: one layer's pool, without the dimension
   long long layer_stride;
-  const at::Tensor *k, *table;
+  const at::Tensor *k, *v, *table;
 };
 
 // Pools [num_pages, Hkv, page_size, d], or with layers in front, in any strides
@@ -145,6 +145,7 @@ Cache cache_of(PyObject* kp, PyObject* vp, PyObject* tp) {
   r.c.page_stride = n[0] > 1 ? s[0] : std::max<int64_t>(n[1] * n[2] * n[3], 8);
   r.B = static_cast<int>(t.size(0));
   r.k = &k;
+  r.v = &v;
   r.table = &t;
   return r;
 }
@@ -230,13 +231,22 @@ PyObject* again(PyObject* o) {
   return o;
 }
 
+// A tensor that the call writes in place: autograd's count of its versions moves
+// on, so that a graph that saved it finds out. (Inference tensors have none.)
+void written(const at::Tensor& t) {
+  if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // An output: the one given (checked by the caller), or a new tensor.
 struct Out {
   at::Tensor t;
   PyObject* given;  // borrowed, or NULL
   PyObject* result() const { return given ? again(given) : wrap(t); }
   void keep(const Place& place) const {
-    if (!given) place.allocated(t);
+    if (given)
+      written(t);
+    else
+      place.allocated(t);
   }
 };
 
@@ -380,6 +390,8 @@ PyObject* append(PyObject* const* a) {
                         v.data_ptr(), vs, &c.c, cu, lens, pos, turns.data_ptr<double>(), c.B, Hq,
                         total, rot, amp, truth(a[10]) ? 1 : 0, place.stream);
   if (code != ATTN_OK) return PyLong_FromLong(code);
+  written(*c.k);
+  written(*c.v);
   o.keep(place);
   return o.result();
 }
@@ -401,6 +413,8 @@ PyObject* update(PyObject* const* a) {
                         source, add, t.t.data_ptr<int32_t>(), l.t.data_ptr<int32_t>(),
                         r.t.data_ptr<int32_t>(), info.t.data_ptr<int32_t>(), c.B, place.stream);
   if (code != ATTN_OK) return PyLong_FromLong(code);
+  written(*c.k);
+  written(*c.v);
   for (const Out* x : {&t, &l, &r, &info}) x->keep(place);
   return give({t.result(), l.result(), r.result(), info.result()});
 }
@@ -419,6 +433,8 @@ PyObject* compact(PyObject* const* a) {
                         t.t.data_ptr<int32_t>(), r.t.data_ptr<int32_t>(),
                         info.t.data_ptr<int32_t>(), c.B, place.stream);
   if (code != ATTN_OK) return PyLong_FromLong(code);
+  written(*c.k);
+  written(*c.v);
   for (const Out* x : {&t, &r, &info}) x->keep(place);
   return give({t.result(), r.result(), info.result()});
 }
