@@ -80,6 +80,56 @@ def attn_rope_turns(rot: int, base: float = 10000.0, scaling: str = "none", fact
     return torch.tensor(list(buf), dtype=torch.float64), amp.value
 
 
+class _Rope(torch.autograd.Function):
+    """The rotation in an autograd graph: linear, with the rotation back as its gradient
+    (whose own gradient is the rotation again)."""
+
+    @staticmethod
+    def forward(ctx, q, k, pos, turns, amp, interleaved, back, name):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(pos, turns)
+        ctx.how = amp, interleaved, not back, name
+        return _done(_binding.rope(q, k, pos, turns, amp, interleaved, None, None, back, None), name)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        out = [None] * 8
+        asked = [i for i in (0, 1) if grads[i] is not None and ctx.needs_input_grad[i]]
+        if asked:
+            x = [_plain(grads[i]) for i in asked] + [None]
+            for i, g in zip(asked, _Rope.apply(x[0], x[1], *ctx.saved_tensors, *ctx.how)):
+                out[i] = g
+        return tuple(out)
+
+
+def _plain(g):
+    """g as the operator takes it: d innermost, strides of whole 16-byte units."""
+    n, s = g.shape, g.stride()
+    fits = s[3] == 1 and not any(t % 8 for t, m in zip(s[:3], n) if m > 1) and g.data_ptr() % 16 == 0
+    return g if fits else g.clone(memory_format=torch.contiguous_format)
+
+
+def _rope(q, k, pos, turns, amp, interleaved, q_out, k_out, back, stream, name):
+    stream = _stream(stream)
+    if not (torch.is_grad_enabled() and any(isinstance(x, torch.Tensor) and x.is_cuda and x.requires_grad
+                                            for x in (q, k, q_out, k_out))):
+        return _done(_binding.rope(q, k, pos, turns, amp, interleaved, q_out, k_out, back, stream), name)
+    if q_out is not None or k_out is not None:
+        raise ValueError("an output cannot be given where a gradient is recorded "
+                         "(under torch.no_grad() it can)")
+    args = (q, k, pos, turns, amp, interleaved, back, name)
+    if stream is None:
+        return _Rope.apply(*args)
+    # Current while the graph is recorded, so that the gradient runs on it too.
+    here, dev = torch.cuda.current_stream(q.device), q.device
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)):
+        out = _Rope.apply(*args)
+    for t in out:
+        if t is not None:
+            t.record_stream(here)
+    return out
+
+
 def attn_rope(q, k, pos, turns, amp: float = 1.0, interleaved: bool = False, q_out=None,
               k_out=None, stream=None) -> Tuple:
     """Rotary positions of q [B, Hq, N, d] and k [B, Hkv, N, d] (or None), bf16 or fp16.
@@ -87,17 +137,17 @@ def attn_rope(q, k, pos, turns, amp: float = 1.0, interleaved: bool = False, q_o
     Any strides with d innermost; an output may be its input, and is laid out
     like it if none is given. pos int32 [N] or [B, N]; turns and amp from
     ``attn_rope_turns`` (turns on q's device): the first 2 * len(turns) values of
-    each head are rotated. Returns (q_out, k_out).
+    each head are rotated. Returns (q_out, k_out). Where q or k requires a
+    gradient it is recorded, and no output can be given. (The library's attention
+    records none: for a gradient through it, bring your own.)
     """
-    return _done(_binding.rope(q, k, pos, turns, amp, interleaved, q_out, k_out, False,
-                               _stream(stream)), "attn_rope")
+    return _rope(q, k, pos, turns, amp, interleaved, q_out, k_out, False, stream, "attn_rope")
 
 
 def attn_rope_bwd(dq, dk, pos, turns, amp: float = 1.0, interleaved: bool = False, dq_in=None,
                   dk_in=None, stream=None) -> Tuple:
     """Gradients of ``attn_rope``'s inputs from those of its outputs (same arguments)."""
-    return _done(_binding.rope(dq, dk, pos, turns, amp, interleaved, dq_in, dk_in, True,
-                               _stream(stream)), "attn_rope")
+    return _rope(dq, dk, pos, turns, amp, interleaved, dq_in, dk_in, True, stream, "attn_rope_bwd")
 
 
 def attn_rope_append(q, k, v, kpages, vpages, table, cu_q, kv_lens, turns, amp: float = 1.0,
