@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -49,18 +50,52 @@ def up_to_date(out: str = OUT, deps=None) -> bool:
     return all(os.path.getmtime(d) <= t for d in (DEPS if deps is None else deps))
 
 
+def torch_dir():
+    """Where torch is installed (found, not imported), or None."""
+    spec = importlib.util.find_spec("torch")
+    return None if spec is None else list(spec.submodule_search_locations)[0]
+
+
+def torch_build(torch: str):
+    """(version, C++ ABI) of the torch installed there, from its own files. Where they do
+    not name the ABI it is the C++11 one, the only one that current builds have."""
+    with open(os.path.join(torch, "version.py")) as f:
+        version = re.search(r"__version__ = '([^']+)'", f.read())
+    if version is None:
+        raise RuntimeError("version.py of torch does not say which one it is")
+    config, abi = os.path.join(torch, "share", "cmake", "Torch", "TorchConfig.cmake"), None
+    if os.path.exists(config):
+        with open(config) as f:
+            abi = re.search(r"_GLIBCXX_USE_CXX11_ABI=([01])", f.read())
+    return version.group(1), int(abi.group(1)) if abi else 1
+
+
+def binding_key(version: str, abi: int) -> str:
+    """What a build of the binding is good for; compiled into it."""
+    return f"eta binding for torch {version}, C++ ABI {int(abi)}, {sysconfig.get_config_var('SOABI')};"
+
+
+def binding_up_to_date(key: str, out: str = BINDING_OUT) -> bool:
+    if not up_to_date(out, BINDING_DEPS):
+        return False
+    with open(out, "rb") as f:
+        return key.encode() in f.read()
+
+
 def build_binding(force: bool = False, verbose: bool = False):
-    """``_binding.so`` against the installed torch; None where there is none."""
-    if not force and up_to_date(BINDING_OUT, BINDING_DEPS):
-        return BINDING_OUT
-    spec = importlib.util.find_spec("torch")  # (found, not imported)
-    if spec is None:
+    """``_binding.so`` against the installed torch; None where there is none. Built anew
+    where the one there is older than its sources or was built for another torch."""
+    torch = torch_dir()
+    if torch is None:
         return None
-    torch = list(spec.submodule_search_locations)[0]
+    version, abi = torch_build(torch)
+    key = binding_key(version, abi)
+    if not force and binding_up_to_date(key):
+        return BINDING_OUT
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
     inc = os.path.join(torch, "include")
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
-           "-D_GLIBCXX_USE_CXX11_ABI=1", "-isystem", inc,
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wextra",
+           f"-D_GLIBCXX_USE_CXX11_ABI={abi}", f'-DETA_BINDING_KEY="{key}"', "-isystem", inc,
            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
            "-o", BINDING_OUT + ".tmp", BINDING_SRC, "-L", os.path.join(torch, "lib"),
@@ -70,6 +105,8 @@ def build_binding(force: bool = False, verbose: bool = False):
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    if res.stderr:
+        print(res.stderr, file=sys.stderr)  # (warnings)
     os.replace(BINDING_OUT + ".tmp", BINDING_OUT)
     return BINDING_OUT
 

@@ -26,6 +26,11 @@
 
 #include "../../include/attn.h"
 
+// The torch, C++ ABI and Python that this build is for (build.py).
+#ifndef ETA_BINDING_KEY
+#error "build.py compiles this file"
+#endif
+
 namespace {
 
 struct BadArgument : std::runtime_error {
@@ -498,4 +503,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", ETA_BINDING_KEY) != 0) {
+    Py_DECREF(m);
+    m = nullptr;
+  }
+  return m;
+}

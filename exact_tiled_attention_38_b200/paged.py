@@ -14,12 +14,23 @@ from typing import Optional, Tuple
 import torch  # (the compiled module needs its libraries)
 
 from . import _D, _F, AttnError, _check, _stream_handle, load_library
+from .build import binding_key
 
 try:
     from . import _binding
 except ImportError as e:
-    raise RuntimeError("the compiled binding is not built; run "
+    raise RuntimeError("the compiled binding is not built, or not for this torch; run "
                        "`python -m exact_tiled_attention_38_b200.build`") from e
+
+
+def _check_build(built_for):
+    key = binding_key(torch.__version__, torch._C._GLIBCXX_USE_CXX11_ABI)
+    if built_for != key:
+        raise RuntimeError(f"the compiled binding is another one's ({built_for} here is {key}); run "
+                           "`python -m exact_tiled_attention_38_b200.build`")
+
+
+_check_build(_binding.built_for)
 
 
 def _init():
