@@ -193,7 +193,10 @@ def attn_pages_compact(kpages, vpages, table, lens, refs, table_out=None, refs_o
     """Move the live pages to the lowest indices, in every layer, with the fewest copies.
 
     Arguments as in ``attn_pages_update``. Returns (table, refs, info) of the next
-    state; info [2]: live pages, moved pages.
+    state; info [2]: live pages, moved pages. Pages held from outside move too: with
+    n = (refs > 0).sum() of the counts before, the k-th of those at n and above is
+    now the k-th page that was free below n (a holder with a row of its own in the
+    table need not ask).
     """
     return _done(_binding.compact(kpages, vpages, table, lens, refs, table_out, refs_out, info,
                                   _stream(stream)), "attn_pages_compact")

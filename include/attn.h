@@ -456,6 +456,10 @@ int attn_pages_update(const attn_pages* cache, int layers, long long layer_strid
  * in order, into the free pages below n, in order -- the fewest copies -- in
  * all layers of both pools; the tables and counts follow. info [2]: n, and the
  * pages moved. Other arguments as in attn_pages_update.
+ * A page that no row holds but someone else pins (refs counts it) moves like the
+ * others. Its holder finds it by the rule above, from the counts before: the
+ * k-th page with refs > 0 at n and above is now the k-th page that had refs <= 0
+ * below n. Or it keeps the page in a row of the table, which follows by itself.
  */
 int attn_pages_compact(const attn_pages* cache, int layers, long long layer_stride,
                        const int32_t* lens, const int32_t* refs, int32_t* table_out,
