@@ -110,16 +110,16 @@ struct Cfg {
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kKVOff = NQT * kTileBytes;
-  static constexpr int kStgWarpBytes = 32 * 128;
-  static constexpr int kStgOff = kKVOff + kStages * kTileBytes;
-  static constexpr int kBarOff = kStgOff + 8 * kStgWarpBytes;
+  // The inline plan's prefix sums (8 and 4 bytes a sequence), and once it is made
+  // what the warps of group 1 hand over of their rows: (m, l), 256 bytes a warp.
+  static constexpr int kScratchOff = kKVOff + kStages * kTileBytes;
+  static constexpr int kScratchBytes = ((kInlineB + 1) * 12 + 15) / 16 * 16;
+  static_assert(kScratchBytes >= 4 * 256, "exchange");
+  static constexpr int kBarOff = kScratchOff + kScratchBytes;
   // kv_full[S], kv_empty[S], q_full[2], q_empty[2], s_ready[2], p_ready[2],
   // o_done[2], s_free[2], pv_done[2], x_up, x_down, drain
   static constexpr int kNumBars = 2 * kStages + 7 * NQT + 3;
   static constexpr int kCtlOff = kBarOff + kNumBars * 8;
-  // A warp of group 1 hands its rows' (m, l) over where it stages output at other
-  // times. (Its own place: its neighbours may still be storing the last piece's.)
-  static constexpr int kXOff = kStgOff + 4 * kStgWarpBytes;
   static constexpr int kWalkOff = kCtlOff + 64;  // each warp's way through the range
   static constexpr int kSmemBytes = kWalkOff + 10 * 104 + 1024;  // + runtime 1024-byte alignment
   static constexpr uint32_t kTmemCols = 512;
@@ -131,8 +131,6 @@ struct Cfg {
   __host__ __device__ static constexpr uint32_t o_col(int t) {
     return kOwnP ? 256u * t + BN + 64u : 2 * BN + D * t;
   }
-  // The inline plan's prefix sums lie where the output is staged later.
-  static_assert((kInlineB + 1) * 12 <= 8 * kStgWarpBytes, "plan scratch");
   static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
@@ -732,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane < p.B) check_seq(p.cu_q, p.lens, lane, p.total_q, p.max_q, p.capacity());
     }
   } else if (p.inline_plan) {
-    long long* rest_at = reinterpret_cast<long long*>(smem + C::kStgOff);
+    long long* rest_at = reinterpret_cast<long long*>(smem + C::kScratchOff);
     int* chunk_at = reinterpret_cast<int*>(rest_at + p.B + 1);
     h = make_plan<kThreads>(p, rest_at, chunk_at,
                                        reinterpret_cast<long long*>(smem + C::kWalkOff), c == 0);
@@ -745,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (threadIdx.x == 0) p.plan.starts[c] = st;  // for the gather, as is the head
     }
     if (c == 0 && threadIdx.x == 0) *p.plan.head = h;
-    __syncthreads();  // the scratch is free for the softmax warps
+    __syncthreads();  // the scratch is free for the exchange of the softmax warps
   } else {
     h = *p.plan.head;
     work = c < h.ctas;
@@ -1134,8 +1132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool two = w.two(p);
       const bool shared = !two && w.steps() > 1;  // group 1 has a part of the same rows
       const int r = (warp & 3) * 32 + lane;       // row of the tile
-      float2* xrow =
-          reinterpret_cast<float2*>(smem + C::kXOff + (warp & 3) * C::kStgWarpBytes) + lane;
+      float2* xrow = reinterpret_cast<float2*>(smem + C::kScratchOff) + r;
       if (!two && t == 1) {
         if (shared) {
           // Hand (m, l) to group 0 and wait until it has read O_1.
