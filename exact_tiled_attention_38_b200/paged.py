@@ -63,8 +63,9 @@ def attn_paged(q, kpages, vpages, table, cu_q, kv_lens, max_q: Optional[int] = N
     [num_pages, Hkv, page_size, d], table [B, width], cu_q [B + 1] and kv_lens [B]
     int32: sequence b's new tokens are rows cu_q[b]:cu_q[b + 1] of q, the last of
     its kv_lens[b] cached positions, causal, with a sliding window if given.
-    max_q bounds the new tokens of any sequence (default: total). Returns
-    (o [total, Hq, d], lse [total, Hq]). Runs ``attn_paged`` / ``attn_paged_f16``.
+    max_q bounds the new tokens of any sequence; the default, total, is slower where
+    they are few (give 1 for a decode batch). Returns (o [total, Hq, d],
+    lse [total, Hq]). Runs ``attn_paged`` / ``attn_paged_f16``.
     """
     return _done(_binding.paged(q, kpages, vpages, table, cu_q, kv_lens, max_q, window, scale, o,
                                 lse, want_lse, _stream(stream)), "attn_paged")

@@ -305,11 +305,18 @@ typedef struct attn_pages {
  *        of 8, >= Hq * d: q may be a part of a wider projection)
  *   o    [total_q][Hq][d] contiguous     lse [total_q][Hq] float32, or NULL
  *        (neither over q nor over the other: ATTN_ERR_INVALID)
- *   max_q: no sequence has more new tokens than this.
+ *   max_q: no sequence has more new tokens than this. It decides which kernel
+ *        runs, so a loose bound costs time: with 1 for 64 sequences of a token
+ *        each, 1K-8K cached, 32/8 heads, the decode pass takes 190 us where whole
+ *        row tiles, which 64 would choose, take 207.
  *   window: 0 for none.
  * The keys and values of the new tokens must be in the cache already
  * (attn_rope_append puts them there). A token that sees no key gets o = 0,
  * lse = -inf; rows of o and lse outside every sequence are left as they were.
+ * The probabilities are rounded to q's type before the value product (d <= 128),
+ * as in attn_fwd and attn_decode: besides the rounding of o itself, o is off by
+ * at most half a step of that type times sum_j softmax_j |v_j| (fp16, whose steps
+ * below 2^-14 no longer shrink: and by 2^-25 max_j softmax_j sum_j |v_j|).
  * A NaN or +infinite score at a key that a token sees makes its o and lse NaN;
  * keys with a score of -infinity do not count, and a token that sees no other
  * key is one that sees none.
