@@ -63,6 +63,12 @@
 // sustained rate); 9 sequences of up to 301 tokens under a window of 4096, 16/2
 // heads, d = 64 55 us.
 //
+// Scores, maxima, sums and outputs are held in 32 bits. Probabilities are rounded
+// to the input's type for the value product, whose operands have 16 bits; the sum
+// takes them unrounded. That puts o up to half a step times sum p |v| off, as much
+// as the rounding of o itself (bf16, root mean square over all of o: 2.3e-3 of its
+// size, where rounding o alone would give 1.7e-3).
+//
 // Rows of V behind the sequence's last key, and under a window those in front
 // of the first key that any row of the item sees, are set to zero in shared
 // memory before the product: their probabilities are zero, but what lies there
@@ -210,7 +216,9 @@ __device__ __forceinline__ long long div_pos(long long n, long long d) {
 
 // Costs are counted in thirds of a pair's step. A step with one tile of rows
 // takes two of them (measured at d = 128: 3,550 cycles against 2,350, which is
-// what its keys and values take to arrive).
+// what its keys and values take to arrive; at d = 64, counted as two / as three:
+// 48 mixed sequences of 1-64 tokens 122 / 136 us, tiles of 70-90 tokens of group 4
+// 149 / 158, chunks of 128-512 168 / 172, prompts of 2K 89.3 / 88.6).
 constexpr int kPairCost = 3, kSingleCost = 2;
 __device__ __forceinline__ int step_cost(const Params& p, int T, int pair) {
   return pair * NQT * p.tt + p.tt < T ? kPairCost : kSingleCost;
@@ -294,7 +302,8 @@ __device__ __forceinline__ Head make_plan(const Params& p, long long* rest_at, i
   // Keys and values beyond half of L2 will not stay in it between two CTAs
   // that come by at different times (1024 tokens over 64K, 268 MB: 877 us with
   // chunks, 1020 us without; over 20K, 82 MB: 291 / 300 us; below, 49 MB, the
-  // two differ by less than runs do).
+  // two differ by less than runs do. At d = 64, over 64K, 134 MB: 719 / 705 us;
+  // over 40K, 82 MB, 453 / 453; over 24K, 49 MB, 273 / 276).
   const bool chunked = keys * p.Hkv * p.d * 4 > p.l2_bytes / 2;
   for (int b = b_first; b < p.B; b += b_step) {
     const Seq s = load_seq(p.cu_q, p.lens, b, p.total_q, p.max_q, p.capacity());

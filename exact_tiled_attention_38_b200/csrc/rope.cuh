@@ -20,7 +20,7 @@
 // with 16-byte loads. Measured on B200, of the 6554 GB/s of a copy: q and k of
 // 4 x 16 + 16 heads x 2048 x 128 24.9 us (0.82; all launches of this length
 // lose about 4 us at both ends), 32 + 8 heads x 32768 x 64 55.7 us (0.92), an
-// append of 9 chunks of up to 1801 tokens 51.7 us (0.85).
+// append of 9 chunks of up to 1801 tokens 50.9 us (0.86).
 #pragma once
 
 #include "paged_common.cuh"
