@@ -356,6 +356,13 @@ def attn_get_device_status(stream=None) -> Tuple[int, int]:
 
 
 # ---------------------------------------------------------------- paged cache
+def _binding_key(version: str, abi: int) -> str:
+    """What a build of the compiled binding is good for; build.py compiles it in."""
+    import sysconfig
+
+    return f"eta binding for torch {version}, C++ ABI {int(abi)}, {sysconfig.get_config_var('SOABI')};"
+
+
 # These calls live in paged.py, which needs torch as it is imported; this module
 # does not, so that the library can be built without it.
 _PAGED_CALLS = ("attn_paged", "attn_rope_turns", "attn_rope", "attn_rope_bwd", "attn_rope_append",

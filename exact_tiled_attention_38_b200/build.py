@@ -14,6 +14,8 @@ import subprocess
 import sys
 import sysconfig
 
+from . import _binding_key as binding_key
+
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 SRC = os.path.join(PKG_DIR, "csrc", "attn_lib.cu")
@@ -68,11 +70,6 @@ def torch_build(torch: str):
         with open(config) as f:
             abi = re.search(r"_GLIBCXX_USE_CXX11_ABI=([01])", f.read())
     return version.group(1), int(abi.group(1)) if abi else 1
-
-
-def binding_key(version: str, abi: int) -> str:
-    """What a build of the binding is good for; compiled into it."""
-    return f"eta binding for torch {version}, C++ ABI {int(abi)}, {sysconfig.get_config_var('SOABI')};"
 
 
 def binding_up_to_date(key: str, out: str = BINDING_OUT) -> bool:

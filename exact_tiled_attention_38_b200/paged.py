@@ -13,8 +13,7 @@ from typing import Optional, Tuple
 
 import torch  # (the compiled module needs its libraries)
 
-from . import _D, _F, AttnError, _check, _stream_handle, load_library
-from .build import binding_key
+from . import _D, _F, AttnError, _binding_key, _check, _stream_handle, load_library
 
 try:
     from . import _binding
@@ -24,7 +23,7 @@ except ImportError as e:
 
 
 def _check_build(built_for):
-    key = binding_key(torch.__version__, torch._C._GLIBCXX_USE_CXX11_ABI)
+    key = _binding_key(torch.__version__, torch._C._GLIBCXX_USE_CXX11_ABI)
     if built_for != key:
         raise RuntimeError(f"the compiled binding is another one's ({built_for} here is {key}); run "
                            "`python -m exact_tiled_attention_38_b200.build`")

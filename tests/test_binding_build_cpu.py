@@ -48,3 +48,22 @@ def test_what_torchs_files_say(tmp_path):
     config.mkdir(parents=True)
     (config / "TorchConfig.cmake").write_text('set(TORCH_CXX_FLAGS "-D_GLIBCXX_USE_CXX11_ABI=0")\n')
     assert eta_build.torch_build(str(tmp_path)) == ("1.2.3+cu1", 0)
+
+
+def test_no_sources_are_needed_to_run(tmp_path):
+    """The package's Python files and built libraries are enough."""
+    import subprocess
+    import sys
+
+    eta_build.build()
+    pkg = os.path.dirname(eta.__file__)
+    to = tmp_path / os.path.basename(pkg)
+    to.mkdir()
+    for f in os.listdir(pkg):
+        if f.endswith((".py", ".so")) and f != "build.py":
+            shutil.copy(os.path.join(pkg, f), to)
+    code = ("import exact_tiled_attention_38_b200 as e, os; assert os.path.dirname(e.__file__) == os.environ['AT']; "
+            "print(e.attn_rope_turns(8)[1], e.attn_paged.__name__)")
+    out = subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True,
+                         env={**os.environ, "PYTHONPATH": str(tmp_path), "AT": str(to)})
+    assert out.returncode == 0 and out.stdout.split() == ["1.0", "attn_paged"], out.stderr
