@@ -93,3 +93,19 @@ def test_the_same_results_and_the_current_stream_as_it_was(lib):
         torch.cuda.synchronize()
         for got in out:
             assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("op", ["paged", "rope", "append", "update", "compact"])
+def test_captured_with_the_stream_given(lib, op):
+    """In a capture, with the capturing stream given by argument or not: the graph's own memory."""
+    call, _ = setup(lib, op)
+    want = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(torch.cuda.current_stream()) + call(None)
+    for t in out:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want + want))
