@@ -200,10 +200,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Params p) {
     // The batch is checked while the values are on their way, by the first CTAs of
     // the last heads (64 tokens, device time: 3.68 us, as without the check; by those
     // of the first heads 3.86 us, at the kernel's end 4.07 us).
-    const unsigned checkers = min(gridDim.x, 64u);
-    if (blockIdx.y == gridDim.y - 1 && blockIdx.x < checkers) {
+    const unsigned check_ctas = min(gridDim.x, 64u);
+    if (blockIdx.y == gridDim.y - 1 && blockIdx.x < check_ctas) {
       const int total = static_cast<int>(p.tokens);
-      for (unsigned b = blockIdx.x * kThreads + tid; b < static_cast<unsigned>(p.B); b += checkers * kThreads)
+      for (unsigned b = blockIdx.x * kThreads + tid; b < static_cast<unsigned>(p.B); b += check_ctas * kThreads)
         paged::check_seq(p.cu_q, p.lens, static_cast<int>(b), total, total, p.cache.capacity());
     }
     // One warp per token: its sequence, its position, its page.
